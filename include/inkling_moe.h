@@ -462,6 +462,147 @@ int32_t moe_dense_prenorm_kernel_count(const moe_dense_desc_t* desc);
 moe_status_t moe_convert_bf16_to_f16(int64_t n, const void* src, void* dst, int32_t* nonfinite,
                                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * Training operators of the expert block: the pieces of its backward pass
+ * (the pages give the forward modules; their gradients follow from the same
+ * formulas).  A training step runs moe_route and moe_permute (with x_perm),
+ * then moe_grouped_matmul (gate_up), moe_swiglu_checkpoint,
+ * moe_grouped_matmul (down, fp32 rows) and moe_combine; backward,
+ * moe_permute's row copy of the output gradient, the products' two
+ * gradients around moe_swiglu_backward, and moe_combine over the fp32 input
+ * gradient rows; the norms' gradients close the block.  Conventions as
+ * above.
+ * ---------------------------------------------------------------------- */
+typedef enum { MOE_ELEM_F32 = 0, MOE_ELEM_BF16 = 1, MOE_ELEM_F16 = 2 } moe_elem_t;
+
+/* Sizes of a matrix product grouped by expert over W [E, n, k] (the
+ * checkpoint's [out_features, in_features]). */
+typedef struct {
+  int64_t rows;       /* R: rows of the row operands (capacity; < 2^31) */
+  int32_t n_groups;   /* E, 1..1024 */
+  int32_t n, k;       /* out and in features */
+  int32_t dtype;      /* moe_elem_t of every operand */
+  int32_t out_dtype;  /* moe_elem_t of the output: dtype, or MOE_ELEM_F32 */
+} moe_grouped_desc_t;
+
+/* Workspace bytes of the three products below.  Its head is the status word:
+ * initialise it once with moe_workspace_init(). */
+moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* bytes);
+
+/*
+ * moe_grouped_matmul / _dgrad / _wgrad — products over ragged row groups.
+ * Rows [expert_offsets[e], expert_offsets[e+1]) belong to expert e
+ * (moe_permute's offsets); groups may be empty.  Accumulation is in fp32,
+ * each output is rounded once.
+ *   moe_grouped_matmul        out[r] = a[r] @ W[e]^T      a [R, k], out [R, n]
+ *   moe_grouped_matmul_dgrad  da[r]  = dout[r] @ W[e]     dout [R, n], da [R, k]
+ *   moe_grouped_matmul_wgrad  dW[e]  = dout_e^T @ a_e     dW [E, n, k]
+ * Rows at and past expert_offsets[E] are not computed and not written; what
+ * they hold (NaN too) reaches no result.  An expert without rows gets
+ * dW[e] = 0.  With accumulate != 0 (out_dtype MOE_ELEM_F32 only, else
+ * MOE_ERR_INVALID_ARG) dW[e] += dout_e^T @ a_e, and an expert without rows
+ * keeps its dW[e].  Results are the same on every run.
+ * Offsets that decrease or leave [0, R] are recorded in the status word
+ * (MOE_ERR_DEVICE_CHECK) and read as the nearest valid ones.
+ * bf16 and fp16 operands with n % 8 == 0 and k % 8 == 0 run on the tensor
+ * cores; fp32 operands and other sizes on the CUDA cores.  Outputs must not
+ * overlap operands.  R = 0: the first two launch nothing; the third still
+ * reads expert_offsets and writes dW.
+ */
+moe_status_t moe_grouped_matmul(const moe_grouped_desc_t* desc, const void* a, const void* w,
+                                const int32_t* expert_offsets, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+moe_status_t moe_grouped_matmul_dgrad(const moe_grouped_desc_t* desc, const void* dout,
+                                      const void* w, const int32_t* expert_offsets, void* da,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+moe_status_t moe_grouped_matmul_wgrad(const moe_grouped_desc_t* desc, const void* dout,
+                                      const void* a, const int32_t* expert_offsets, void* dw,
+                                      int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * moe_swiglu_checkpoint — the experts' activation over gate_up rows that a
+ * grouped product wrote, keeping an 8-bit checkpoint of those rows for
+ * moe_swiglu_backward (half the bytes of bf16 rows, a quarter of fp32).
+ *   gu [R, 2I] dtype, columns interleaved [g0, u0, g1, u1, ...]
+ *   h[r, j]  = w * silu(g_j) * u_j          [R, I] dtype, w the row's weight:
+ *              topk_w[perm_slot[r]]; topk_w[r] with perm_slot NULL; 1 with
+ *              topk_w NULL
+ *   q [R, 2I] e4m3, scale [R, I/16] bytes: every 32 consecutive columns
+ *              share one scale 2^(b - 127), b the least byte in [0, 254] with
+ *              amax <= 448 * 2^(b - 127) (amax over the block's finite
+ *              values), and q = x / 2^(b - 127) rounded to nearest even.  A
+ *              value that is not finite becomes e4m3 NaN.  h comes from gu,
+ *              not from q.
+ *   expert_offsets [n_groups + 1] or NULL: rows at and past
+ *              expert_offsets[n_groups] are left alone; NULL: all R rows.
+ * dtype MOE_F32 or MOE_BF16; I % 16 == 0 (else MOE_ERR_UNSUPPORTED);
+ * perm_slot and topk_w have R entries.  A slot outside [0, R) is recorded in
+ * the status word and its row takes weight 0.  workspace: at least 256 bytes
+ * whose head is an initialised status word.
+ */
+moe_status_t moe_swiglu_checkpoint(int64_t rows, int32_t intermediate, moe_dtype_t dtype,
+                                   const void* gu, int32_t n_groups, const int32_t* expert_offsets,
+                                   const int32_t* perm_slot, const float* topk_w, void* h, void* q,
+                                   uint8_t* scale, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * moe_swiglu_backward — gradients of moe_swiglu_checkpoint's h, with g and u
+ * read back from the checkpoint (exact products of q and its scale):
+ *   s = 1 / (1 + e^-g),  a = g s
+ *   dgu[r, 2j] = w dh u s (1 + g (1 - s)),  dgu[r, 2j+1] = w dh a   [R, 2I]
+ *   d_topk_w[slot(r)] = sum_j dh a u          [R] fp32, or NULL; a slot that
+ *                       holds no row gets 0
+ *   h[r, j] = w a u                           [R, I] dtype, or NULL (the
+ *                       activation again, for the down product's weight
+ *                       gradient, so that the forward need not keep it)
+ *   dh [R, I] dtype; the other arguments as above.  perm_slot must not hold
+ * a slot twice (moe_permute's does not).
+ */
+moe_status_t moe_swiglu_backward(int64_t rows, int32_t intermediate, moe_dtype_t dtype,
+                                 const void* q, const uint8_t* scale, const void* dh,
+                                 int32_t n_groups, const int32_t* expert_offsets,
+                                 const int32_t* perm_slot, const float* topk_w, void* dgu,
+                                 float* d_topk_w, void* h, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * moe_layer_norm — out[t] = (x[t] - mean) * r * weight + bias with
+ * r = 1 / sqrt(var + eps) over rows of H elements (var divides by H);
+ * weight, bias [H] and x, out [T, H] in `dtype` (MOE_F32, MOE_BF16); bias
+ * may be NULL; out may equal x.  Any H >= 1.  Statistics in fp32, the
+ * variance summed around the mean.  T = 0 launches nothing.
+ */
+moe_status_t moe_layer_norm(int64_t num_tokens, int32_t hidden, moe_dtype_t dtype, float eps,
+                            const void* x, const void* weight, const void* bias, void* out,
+                            void* stream);
+
+/* Workspace bytes of the two backward passes below (no status word in it;
+ * nothing to initialise). */
+moe_status_t moe_norm_workspace_size(int64_t num_tokens, int32_t hidden, size_t* bytes);
+
+/*
+ * moe_layer_norm_backward / moe_rmsnorm_backward — gradients of
+ * moe_layer_norm and moe_rmsnorm; the row statistics are computed again
+ * from x (fp32 sums), nothing is kept from the forward pass.  With
+ * x^ = (x - mean) r (RMSNorm: x r) and gy = dout * weight,
+ *   dx      = r (gy - mean(gy) - x^ mean(gy x^)) + dres    (RMSNorm: without
+ *             mean(gy)); dres [T, H] (the residual path's gradient) or NULL
+ *   dweight = sum_t dout x^,  dbias = sum_t dout    [H] fp32, in a fixed order
+ * x, dout, dres, dx [T, H] and weight [H] in `dtype`; dbias may be NULL.
+ * dx may equal dout or dres.  T = 0 writes zero dweight and dbias.
+ */
+moe_status_t moe_layer_norm_backward(int64_t num_tokens, int32_t hidden, moe_dtype_t dtype,
+                                     float eps, const void* x, const void* weight,
+                                     const void* dout, const void* dres, void* dx, float* dweight,
+                                     float* dbias, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+moe_status_t moe_rmsnorm_backward(int64_t num_tokens, int32_t hidden, moe_dtype_t dtype, float eps,
+                                  const void* x, const void* weight, const void* dout,
+                                  const void* dres, void* dx, float* dweight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 const char* moe_status_string(moe_status_t status);
 int32_t moe_version(void);
 

@@ -57,6 +57,12 @@ class MoEError(RuntimeError):
 
 
 _P = ctypes.c_void_p
+class GroupedDesc(ctypes.Structure):
+    """``moe_grouped_desc_t``."""
+    _fields_ = [("rows", ctypes.c_int64), ("n_groups", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 _DESC = ctypes.POINTER(LayerDesc)
 LIB.moe_status_string.restype = ctypes.c_char_p
 LIB.moe_status_string.argtypes = [ctypes.c_int]
@@ -96,6 +102,27 @@ LIB.moe_forward_prenorm_kernel_count.restype = ctypes.c_int32
 LIB.moe_forward_prenorm_kernel_count.argtypes = [_DESC]
 LIB.moe_dense_prenorm_kernel_count.restype = ctypes.c_int32
 LIB.moe_dense_prenorm_kernel_count.argtypes = [_DDESC]
+_GDESC = ctypes.POINTER(GroupedDesc)
+LIB.moe_grouped_workspace_size.argtypes = [_GDESC, ctypes.POINTER(ctypes.c_size_t)]
+LIB.moe_grouped_matmul.argtypes = [_GDESC, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+LIB.moe_grouped_matmul_dgrad.argtypes = [_GDESC, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+LIB.moe_grouped_matmul_wgrad.argtypes = [_GDESC, _P, _P, _P, _P, ctypes.c_int32, _P,
+                                         ctypes.c_size_t, _P]
+_SWIGLU_HEAD = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
+LIB.moe_swiglu_checkpoint.argtypes = _SWIGLU_HEAD + [_P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P,
+                                                     ctypes.c_size_t, _P]
+LIB.moe_swiglu_backward.argtypes = _SWIGLU_HEAD + [_P, _P, _P, ctypes.c_int32, _P, _P, _P, _P, _P,
+                                                   _P, _P, ctypes.c_size_t, _P]
+_NORM_HEAD = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_float]
+LIB.moe_layer_norm.argtypes = _NORM_HEAD + [_P] * 5
+LIB.moe_norm_workspace_size.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+LIB.moe_layer_norm_backward.argtypes = _NORM_HEAD + [_P] * 8 + [ctypes.c_size_t, _P]
+LIB.moe_rmsnorm_backward.argtypes = _NORM_HEAD + [_P] * 7 + [ctypes.c_size_t, _P]
+for _f in ("moe_grouped_workspace_size", "moe_grouped_matmul", "moe_grouped_matmul_dgrad",
+           "moe_grouped_matmul_wgrad", "moe_swiglu_checkpoint", "moe_swiglu_backward",
+           "moe_layer_norm", "moe_norm_workspace_size", "moe_layer_norm_backward",
+           "moe_rmsnorm_backward"):
+    getattr(LIB, _f).restype = ctypes.c_int
 for _f in ("moe_workspace_size", "moe_workspace_init", "moe_read_device_status", "moe_route",
            "moe_permute", "moe_permute_noalloc", "moe_expert_ffn", "moe_combine", "moe_forward",
            "moe_selftest_wait_timeout", "moe_dense_workspace_size", "moe_dense_mlp",
@@ -557,6 +584,208 @@ def prepare_down_weights(w_down: torch.Tensor, stream=None) -> torch.Tensor:
     if n:
         raise ValueError(f"{n} down-projection weights have no finite fp16 value")
     return out
+
+
+# ------------------------------------------------- training operators
+_ELEM = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+@dataclass(frozen=True)
+class GroupedMatmul:
+    """Sizes of a matrix product grouped by expert: row operands of ``rows``
+    rows, weights ``[E, n, k]``; ``out_dtype`` is ``dtype`` or fp32."""
+    rows: int
+    E: int
+    n: int
+    k: int
+    dtype: torch.dtype = torch.bfloat16
+    out_dtype: Optional[torch.dtype] = None
+
+    def desc(self) -> GroupedDesc:
+        out = self.dtype if self.out_dtype is None else self.out_dtype
+        if self.dtype not in _ELEM or out not in (self.dtype, torch.float32):
+            raise ValueError(f"unsupported dtypes {self.dtype} -> {out}")
+        return GroupedDesc(self.rows, self.E, self.n, self.k, _ELEM[self.dtype], _ELEM[out])
+
+    @property
+    def out(self) -> torch.dtype:
+        return self.dtype if self.out_dtype is None else self.out_dtype
+
+
+def grouped_workspace_size(G: GroupedMatmul) -> int:
+    n = ctypes.c_size_t(0)
+    _check(LIB.moe_grouped_workspace_size(ctypes.byref(G.desc()), ctypes.byref(n)),
+           "moe_grouped_workspace_size")
+    return n.value
+
+
+def _new_workspace(nbytes: int, device, stream) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+    _check(LIB.moe_workspace_init(_wsptr(ws), ws.numel(), _stream(stream)), "moe_workspace_init")
+    return ws
+
+
+def new_grouped_workspace(G: GroupedMatmul, device=None, stream=None) -> torch.Tensor:
+    """Allocate (with torch) and initialise a workspace for the product ``G``."""
+    return _new_workspace(grouped_workspace_size(G), device, stream)
+
+
+def new_status_workspace(device=None, stream=None) -> torch.Tensor:
+    """An initialised workspace of 256 bytes: a status word alone, for
+    ``moe_swiglu_checkpoint`` and ``moe_swiglu_backward``."""
+    return _new_workspace(256, device, stream)
+
+
+def new_norm_workspace(T: int, H: int, device=None) -> torch.Tensor:
+    """Workspace of ``moe_layer_norm_backward`` and ``moe_rmsnorm_backward``
+    (nothing in it needs initialising)."""
+    n = ctypes.c_size_t(0)
+    _check(LIB.moe_norm_workspace_size(T, H, ctypes.byref(n)), "moe_norm_workspace_size")
+    return torch.empty(n.value, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_grouped_matmul(G: GroupedMatmul, a, w, expert_offsets, out, ws, stream=None):
+    """``out[r] = a[r] @ w[e]^T`` for the rows r of each expert e."""
+    _expect(a, "a", (G.rows, G.k), G.dtype)
+    _expect(w, "w", (G.E, G.n, G.k), G.dtype)
+    _expect(expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
+    _expect(out, "out", (G.rows, G.n), G.out)
+    _check(LIB.moe_grouped_matmul(ctypes.byref(G.desc()), _ptr(a), _ptr(w), _ptr(expert_offsets),
+                                  _ptr(out), _wsptr(ws), ws.numel(), _stream(stream)),
+           "moe_grouped_matmul")
+
+
+def moe_grouped_matmul_dgrad(G: GroupedMatmul, dout, w, expert_offsets, da, ws, stream=None):
+    """``da[r] = dout[r] @ w[e]``: the gradient of ``moe_grouped_matmul``'s rows."""
+    _expect(dout, "dout", (G.rows, G.n), G.dtype)
+    _expect(w, "w", (G.E, G.n, G.k), G.dtype)
+    _expect(expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
+    _expect(da, "da", (G.rows, G.k), G.out)
+    _check(LIB.moe_grouped_matmul_dgrad(ctypes.byref(G.desc()), _ptr(dout), _ptr(w),
+                                        _ptr(expert_offsets), _ptr(da), _wsptr(ws), ws.numel(),
+                                        _stream(stream)), "moe_grouped_matmul_dgrad")
+
+
+def moe_grouped_matmul_wgrad(G: GroupedMatmul, dout, a, expert_offsets, dw, ws, accumulate=False,
+                             stream=None):
+    """``dw[e] = dout_e^T @ a_e`` over each expert's rows (``accumulate``, fp32
+    ``dw`` only: added to ``dw[e]``)."""
+    _expect(dout, "dout", (G.rows, G.n), G.dtype)
+    _expect(a, "a", (G.rows, G.k), G.dtype)
+    _expect(expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
+    _expect(dw, "dw", (G.E, G.n, G.k), G.out)
+    _check(LIB.moe_grouped_matmul_wgrad(ctypes.byref(G.desc()), _ptr(dout), _ptr(a),
+                                        _ptr(expert_offsets), _ptr(dw), int(bool(accumulate)),
+                                        _wsptr(ws), ws.numel(), _stream(stream)),
+           "moe_grouped_matmul_wgrad")
+
+
+def _expect_swiglu(R: int, expert_offsets, perm_slot, topk_w) -> int:
+    """Checks of the arguments both SwiGLU entry points share; the number of groups."""
+    _expect(perm_slot, "perm_slot", (R,), torch.int32, allow_none=True)
+    if topk_w is None:
+        if perm_slot is not None:
+            raise ValueError("perm_slot needs topk_w")
+    else:
+        _expect(topk_w.reshape(-1) if topk_w.is_contiguous() else topk_w, "topk_w", (R,), torch.float32)
+    if expert_offsets is None:
+        return 0
+    E = expert_offsets.numel() - 1
+    if E < 1:
+        raise ValueError("expert_offsets must hold E + 1 entries")
+    _expect(expert_offsets, "expert_offsets", (E + 1,), torch.int32)
+    return E
+
+
+def moe_swiglu_checkpoint(gu, expert_offsets, perm_slot, topk_w, h, q, scale, ws, stream=None):
+    """``h = w * silu(g) * u`` of interleaved gate_up rows ``gu`` [R, 2I], and
+    their 8-bit checkpoint: ``q`` [R, 2I] e4m3, ``scale`` [R, I/16] uint8
+    (2^(scale - 127) for 32 columns).  ``expert_offsets`` None: every row is
+    live; ``perm_slot`` None: row r has weight ``topk_w[r]``; both None: 1."""
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("gu must be [R, 2I]")
+    R, I = gu.shape[0], gu.shape[1] // 2
+    code = _dtype_code(gu.dtype)
+    _expect(gu, "gu", (R, 2 * I), gu.dtype)
+    E = _expect_swiglu(R, expert_offsets, perm_slot, topk_w)
+    _expect(h, "h", (R, I), gu.dtype)
+    _expect(q, "q", (R, 2 * I), torch.float8_e4m3fn)
+    _expect(scale, "scale", (R, I // 16), torch.uint8)
+    _check(LIB.moe_swiglu_checkpoint(R, I, code, _ptr(gu), E, _ptr(expert_offsets), _ptr(perm_slot),
+                                     _ptr(topk_w), _ptr(h), _ptr(q), _ptr(scale), _wsptr(ws),
+                                     ws.numel(), _stream(stream)), "moe_swiglu_checkpoint")
+
+
+def moe_swiglu_backward(q, scale, dh, expert_offsets, perm_slot, topk_w, dgu, d_topk_w, h, ws,
+                        stream=None):
+    """Gradients of ``moe_swiglu_checkpoint``'s h from its checkpoint: ``dgu``
+    [R, 2I], ``d_topk_w`` [R] fp32 in slot order (None: not wanted), and ``h``
+    [R, I] again (None: not wanted)."""
+    if dh.dim() != 2:
+        raise ValueError("dh must be [R, I]")
+    R, I = dh.shape
+    code = _dtype_code(dh.dtype)
+    _expect(dh, "dh", (R, I), dh.dtype)
+    _expect(q, "q", (R, 2 * I), torch.float8_e4m3fn)
+    _expect(scale, "scale", (R, I // 16), torch.uint8)
+    E = _expect_swiglu(R, expert_offsets, perm_slot, topk_w)
+    _expect(dgu, "dgu", (R, 2 * I), dh.dtype)
+    if d_topk_w is not None:
+        _expect(d_topk_w.reshape(-1) if d_topk_w.is_contiguous() else d_topk_w, "d_topk_w", (R,),
+                torch.float32)
+    _expect(h, "h", (R, I), dh.dtype, allow_none=True)
+    _check(LIB.moe_swiglu_backward(R, I, code, _ptr(q), _ptr(scale), _ptr(dh), E,
+                                   _ptr(expert_offsets), _ptr(perm_slot), _ptr(topk_w), _ptr(dgu),
+                                   _ptr(d_topk_w), _ptr(h), _wsptr(ws), ws.numel(), _stream(stream)),
+           "moe_swiglu_backward")
+
+
+def moe_layer_norm(x, weight, bias, out, eps: float = 1e-6, stream=None):
+    """Layer norm of ``x`` [T, H] (``bias`` may be None; ``out`` may be ``x``)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    code = _dtype_code(x.dtype)
+    _expect(x, "x", (T, H), x.dtype)
+    _expect(weight, "weight", (H,), x.dtype)
+    _expect(bias, "bias", (H,), x.dtype, allow_none=True)
+    _expect(out, "out", (T, H), x.dtype)
+    _check(LIB.moe_layer_norm(T, H, code, eps, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
+                              _stream(stream)), "moe_layer_norm")
+
+
+def _expect_norm_backward(x, weight, dout, dx, dweight, dres):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    code = _dtype_code(x.dtype)
+    _expect(x, "x", (T, H), x.dtype)
+    _expect(weight, "weight", (H,), x.dtype)
+    _expect(dout, "dout", (T, H), x.dtype)
+    _expect(dres, "dres", (T, H), x.dtype, allow_none=True)
+    _expect(dx, "dx", (T, H), x.dtype)
+    _expect(dweight, "dweight", (H,), torch.float32)
+    return T, H, code
+
+
+def moe_layer_norm_backward(x, weight, dout, dx, dweight, dbias, ws, eps: float = 1e-6, dres=None,
+                            stream=None):
+    """Gradients of ``moe_layer_norm``: ``dx`` (plus ``dres``, the residual
+    path's gradient), ``dweight`` and ``dbias`` (may be None) in fp32; ``ws``
+    from ``new_norm_workspace``."""
+    T, H, code = _expect_norm_backward(x, weight, dout, dx, dweight, dres)
+    _expect(dbias, "dbias", (H,), torch.float32, allow_none=True)
+    _check(LIB.moe_layer_norm_backward(T, H, code, eps, _ptr(x), _ptr(weight), _ptr(dout),
+                                       _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias), _wsptr(ws),
+                                       ws.numel(), _stream(stream)), "moe_layer_norm_backward")
+
+
+def moe_rmsnorm_backward(x, weight, dout, dx, dweight, ws, eps: float = 1e-6, dres=None, stream=None):
+    """Gradients of ``moe_rmsnorm``, as ``moe_layer_norm_backward``."""
+    T, H, code = _expect_norm_backward(x, weight, dout, dx, dweight, dres)
+    _check(LIB.moe_rmsnorm_backward(T, H, code, eps, _ptr(x), _ptr(weight), _ptr(dout), _ptr(dres),
+                                    _ptr(dx), _ptr(dweight), _wsptr(ws), ws.numel(),
+                                    _stream(stream)), "moe_rmsnorm_backward")
 
 
 class InklingMoE:

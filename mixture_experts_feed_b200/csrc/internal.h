@@ -108,4 +108,58 @@ cudaError_t launch_combine(const Layer& L, const void* y_routed, const void* y_s
                            const int32_t* inv_perm, void* out, int32_t* status, int num_sms,
                            cudaStream_t stream);
 
+// Training operators of the expert block.
+// Grouped products out[i, j] = sum_r P[i, r] Q[j, r] over ragged row groups:
+//   kForward  i = row of the group, j = n index, r = k index
+//   kDgrad    i = row of the group, j = k index, r = n index
+//   kWgrad    i = n index, j = k index, r = row of the group
+enum ProductForm { kForward = 0, kDgrad = 1, kWgrad = 2 };
+struct GroupedProduct {
+  int form;
+  int64_t rows;
+  int E, n, k;
+  int dtype, out_dtype;     // moe_elem_t
+  const void* p;            // a (forward), dout (dgrad, wgrad)
+  const void* q;            // w (forward, dgrad), a (wgrad)
+  const int32_t* offsets;
+  void* out;
+  int accumulate;           // kWgrad, fp32 output
+  int32_t* status;
+};
+// grouped_matmul_simt.cu (CUDA cores: fp32 operands, and sizes TMA cannot take)
+cudaError_t launch_grouped_matmul_simt(const GroupedProduct& g, int num_sms, cudaStream_t stream);
+
+// swiglu_checkpoint.cu
+struct SwigluArgs {
+  int64_t rows;
+  int I, dtype;
+  const int32_t* live;      // device count of live rows, or null: all of them
+  const int32_t* perm_slot;
+  const float* topk_w;
+  int32_t* status;
+};
+cudaError_t launch_swiglu_checkpoint(const SwigluArgs& a, const void* gu, void* h, void* q,
+                                     uint8_t* scale, int num_sms, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const SwigluArgs& a, const void* q, const uint8_t* scale,
+                                   const void* dh, void* dgu, float* d_topk_w, void* h,
+                                   int num_sms, cudaStream_t stream);
+
+// norm_train.cu.  Blocks of a backward pass (each keeps one partial row of
+// the weight's and one of the bias's gradient in the workspace).
+constexpr int kNormMaxBlocks = 592;
+cudaError_t launch_layer_norm(int64_t T, int H, int dtype, float eps, const void* x,
+                              const void* weight, const void* bias, void* out, int num_sms,
+                              cudaStream_t stream);
+struct NormBackwardArgs {
+  int64_t T;
+  int H, dtype;
+  bool layer;               // layer norm, else RMSNorm
+  float eps;
+  const void *x, *weight, *dout, *dres;
+  void* dx;
+  float *dweight, *dbias;
+  float* partials;          // [2][kNormMaxBlocks][H]
+};
+cudaError_t launch_norm_backward(const NormBackwardArgs& a, int num_sms, cudaStream_t stream);
+
 }  // namespace moe
