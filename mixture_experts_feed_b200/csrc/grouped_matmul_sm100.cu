@@ -1,0 +1,604 @@
+// Grouped matrix products (moe_grouped_matmul and its two gradients) on the
+// sm_100a tensor cores: out[i, j] = sum_r P[i, r] Q[j, r] for ragged groups
+// of rows, bf16 or fp16 operands, fp32 accumulators in tensor memory.
+//
+//             i (output row)     j (contiguous)    r (summed)
+//   forward   row of the group   n index           k index
+//   dgrad     row of the group   k index           n index
+//   wgrad     n index            k index           row of the group
+//
+// The MMA's M side is j and its N side is i: a CTA pair (tcgen05
+// cta_group::2) computes 256 j x up to 256 i, the accumulator holding the
+// output transposed (lane = j, column = i).  N may be any multiple of 32, so
+// the ragged side pads to 32 rows instead of a whole 128- or 256-row tile: a
+// group of 40 rows costs a 64-wide MMA, a decoded token a 32-wide one, and
+// the weights stream through the M side at full width either way.  A group's
+// rows are cut into ceil(rows / 256) tiles of even height.
+//
+// Operands come by TMA with the 128-byte swizzle in whichever order they lie
+// in memory: r contiguous ("K-major": boxes of 64 r x rows) or j / i
+// contiguous ("MN-major": boxes of 64 j x 64 r, two per tile side), told to
+// the MMA by its descriptors.  No transposed copy exists anywhere.
+//   forward  M: W[e] K-major    N: a K-major
+//   dgrad    M: W[e] MN-major   N: dout K-major
+//   wgrad    M: a MN-major      N: dout MN-major
+//
+// wgrad sums over a group's rows, whose last block of 64 may run into the
+// next group's rows (or rows that belong to nobody, which may hold NaN).
+// That block's loads complete on a barrier of their own CTA; warp 1 of each
+// CTA then overwrites the foreign rows up to the next multiple of 16 with
+// zeros in shared memory, for both operands, and the MMA runs that many
+// 16-row steps.
+//
+// fp32 outputs: the accumulator truncates instead of rounding at every step,
+// so one chain is kept to kChain blocks of 64 (measured: see kChain) and
+// the chains of a tile are added in fp32 by the threads that store it, in
+// order.  16-bit outputs round away far more than that and take one chain.
+//
+// Roles (192 threads a CTA, one CTA an SM): warp 0 loads, warp 1 allocates
+// tensor memory and (rank 0) issues the MMAs, warps 2..5 store; two
+// accumulators let the stores of one tile overlap the MMAs of the next.
+// Every wait is bounded.
+#include <atomic>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int TM = 256;                  // j per tile (a CTA pair; 128 a CTA)
+constexpr int TN = 256;                  // i per tile, at most
+constexpr int BK = 64;                   // r per stage
+constexpr int SIDE_BYTES = 128 * BK * 2; // one operand of a stage in one CTA
+constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
+constexpr int STAGES = 6;
+constexpr int NUM_THREADS = 192;
+constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
+constexpr int kBand = 8;                 // i tiles per band (tile order)
+constexpr int kChain = 16;               // blocks of 64 per accumulation chain, fp32 outputs
+
+struct alignas(64) ProductParams {
+  CUtensorMap tmM;       // M side
+  CUtensorMap tmN[4];    // N side: boxes of 128, 64, 32 and 16 rows (wgrad: [0] alone)
+  const int32_t* offsets;
+  int32_t* status;
+  void* out;
+  int E, rows_cap;
+  int n_i, n_j, n_r;     // sizes of i, j, r (0 where it is the group's rows)
+  int out_f32, out_f16, accumulate;
+  uint32_t fmt;          // operand format bits of the MMA descriptor
+  int chain;             // blocks per accumulation chain
+};
+
+struct Smem {
+  static constexpr int kBars = STAGES * STAGE_BYTES;
+  // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain
+  static constexpr int kNumBars = 3 * STAGES + 5;
+  static constexpr int kMisc = kBars + kNumBars * 8;      // tmem base, abort, bad
+  static constexpr int kTables = kMisc + 16;              // s_off[E + 1], s_tile[E + 1]
+  static int bytes(int E) { return 1024 + kTables + 8 * (E + 1); }
+};
+
+__host__ __device__ __forceinline__ int tiles_over(int n, int t) { return (n + t - 1) / t; }
+
+// Height of a side of `n` cut into tiles of at most TN: even, a multiple of 32.
+__device__ __forceinline__ int even_height(int n) {
+  const int t = tiles_over(n, TN);
+  return (tiles_over(n, t > 0 ? t : 1) + 31) & ~31;
+}
+
+// Warp: s_off = the offsets (clamped to an ascending sequence inside
+// [0, cap] when they are not one), s_tile = exclusive prefix of tile counts.
+template <int FORM>
+__device__ __forceinline__ void build_tables(const ProductParams& p, int* s_off, int* s_tile, int* bad) {
+  const int lane = threadIdx.x & 31;
+  bool wrong = false;
+  for (int i = lane; i <= p.E; i += 32) {
+    const int v = p.offsets[i];
+    const int next = i < p.E ? p.offsets[i + 1] : p.rows_cap;
+    wrong |= v < 0 || v > next || v > p.rows_cap || (i == 0 && v != 0);
+    s_off[i] = v;
+  }
+  __syncwarp();
+  if (__any_sync(0xffffffffu, wrong)) {
+    if (lane == 0) {
+      *bad = 1;
+      int prev = 0;
+      for (int i = 0; i <= p.E; ++i) {
+        int v = i == 0 ? 0 : s_off[i];
+        v = v < prev ? prev : (v > p.rows_cap ? p.rows_cap : v);
+        s_off[i] = v;
+        prev = v;
+      }
+    }
+    __syncwarp();
+  }
+  const int ct = tiles_over(p.n_j, TM);
+  int carry = 0;
+  if (lane == 0) s_tile[0] = 0;
+  for (int base = 0; base < p.E; base += 32) {
+    const int e = base + lane;
+    int cnt = 0;
+    if (e < p.E) {
+      const int rows = s_off[e + 1] - s_off[e];
+      if (FORM == kWgrad) cnt = p.accumulate && rows == 0 ? 0 : tiles_over(p.n_i, TN) * ct;
+      else cnt = tiles_over(rows, TN) * ct;
+    }
+    int incl = cnt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (e < p.E) s_tile[e + 1] = carry + incl;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
+}
+
+struct TileInfo {
+  int e;         // group
+  int row0;      // the group's first row
+  int rows;      // its rows
+  int i0, j0;    // tile origin (i inside the group for forward and dgrad)
+  int ni;        // valid i in the tile
+  int mma_n;     // N of its MMAs: ni rounded up to 32
+  int blocks;    // blocks of 64 r
+};
+
+// Tile `tile` of the launch.  Inside a group the shorter tile side runs
+// innermost (consecutive tiles share the other side's operand from L2); when
+// both are long, bands of kBand i tiles, j by j inside a band.
+template <int FORM>
+__device__ __forceinline__ TileInfo tile_info(int tile, const ProductParams& p, const int* s_off,
+                                              const int* s_tile) {
+  int lo = 0, hi = p.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_tile[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  TileInfo t;
+  t.e = lo;
+  t.row0 = s_off[lo];
+  t.rows = s_off[lo + 1] - s_off[lo];
+  const int n_i = FORM == kWgrad ? p.n_i : t.rows;
+  const int n_r = FORM == kWgrad ? t.rows : p.n_r;
+  const int it = tiles_over(n_i, TN), jt = tiles_over(p.n_j, TM);
+  const int local = tile - s_tile[lo];
+  int i, j;
+  if (it > kBand && jt > kBand) {
+    const int band = local / (kBand * jt);
+    const int in_band = local - band * kBand * jt;
+    const int height = min(kBand, it - band * kBand);
+    j = in_band / height;
+    i = band * kBand + (in_band - j * height);
+  } else if (it > jt) {
+    i = local / jt;
+    j = local - i * jt;
+  } else {
+    j = local / it;
+    i = local - j * it;
+  }
+  const int h = even_height(n_i);
+  t.i0 = i * h;
+  t.j0 = j * TM;
+  t.ni = min(h, n_i - t.i0);
+  t.mma_n = (t.ni + 31) & ~31;
+  t.blocks = tiles_over(n_r, BK);
+  return t;
+}
+
+// Shared-memory descriptor of an MN-major operand written by TMA boxes of 64
+// elements (128 bytes, swizzled) x 64 r, box after box: leading offset = one
+// box (8192 bytes, the next 64 elements), stride offset = 8 r (1024 bytes).
+__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+template <int FORM> struct Majors {
+  static constexpr bool M_MN = FORM != kForward;   // M side MN-major (j contiguous)
+  static constexpr bool N_MN = FORM == kWgrad;     // N side MN-major (i contiguous)
+};
+
+template <int FORM>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    grouped_matmul_kernel(const __grid_constant__ ProductParams p) {
+  constexpr bool M_MN = Majors<FORM>::M_MN, N_MN = Majors<FORM>::N_MN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kBars);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tail = empty + STAGES;       // wgrad: a partial block's loads of this CTA
+  uint64_t* tfull = tail + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::kMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::kMisc + 4);
+  int* s_bad = reinterpret_cast<int*>(smem + Smem::kMisc + 8);
+  int* s_off = reinterpret_cast<int*>(smem + Smem::kTables);
+  int* s_tile = s_off + (p.E + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  const int unit = static_cast<int>(blockIdx.x >> 1);
+  const int units = static_cast<int>(gridDim.x >> 1);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < STAGES; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+        mbar_init(&tail[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&tfull[i], 1);
+        mbar_init(&tempty[i], 8);        // the epilogue warps of both CTAs
+      }
+      mbar_init(drain, 1);
+      *s_abort = 0;
+      *s_bad = 0;
+      fence_mbar_init();
+      fence_proxy_async_smem();
+      prefetch_tmap(&p.tmM);
+      prefetch_tmap(&p.tmN[0]);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    tmem_alloc_pair(s_tmem, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  __syncthreads();                       // *s_bad = 0 before warp 2 may set it
+  pdl_wait();
+  if (warp == 2) build_tables<FORM>(p, s_off, s_tile, s_bad);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                        // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+
+  const uint32_t tmem_base = *s_tmem;
+  const int total = s_tile[p.E];
+  if (threadIdx.x == 0 && *s_bad) record_status(p.status, DEV_BAD_ROW);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t used = 0, last = 0;               // stages loaded, parity of their last load
+      uint32_t tails = 0, tail_par = 0;          // the same for tail[]
+      bool ok = true;
+      for (int tile = unit; tile < total && ok; tile += units) {
+        const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+        const int j = t.j0 + rank * 128;
+        const int half = t.mma_n >> 1;                     // i rows of this CTA
+        const int i = t.i0 + rank * half;
+        const int n_boxes = N_MN ? (half + 63) >> 6 : 0;
+        const uint32_t bytes = SIDE_BYTES + (N_MN ? n_boxes * 8192 : half * (BK * 2));
+        for (int b = 0; b < t.blocks; ++b) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) { ok = false; break; }
+          uint8_t* m_dst = smem + stage * STAGE_BYTES;
+          uint8_t* n_dst = m_dst + SIDE_BYTES;
+          const int r = b * BK;
+          // wgrad: a last block past the group's rows completes on this CTA's own barrier
+          const bool partial = FORM == kWgrad && r + BK > t.rows;
+          uint32_t bar;
+          if (partial) {
+            mbar_arrive_expect_tx(&tail[stage], bytes);
+            bar = mapa_shared(&tail[stage], static_cast<uint32_t>(rank));
+            tails |= 1u << stage;
+            tail_par ^= 1u << stage;                       // set = parity 0 completed last
+          } else {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            bar = mapa_shared(&full[stage], 0);
+          }
+          if (!M_MN) {
+            tma_load_3d_pair(m_dst, &p.tmM, bar, r, j, t.e);
+          } else if (FORM == kDgrad) {
+            tma_load_3d_pair(m_dst, &p.tmM, bar, j, r, t.e);
+            tma_load_3d_pair(m_dst + 8192, &p.tmM, bar, j + 64, r, t.e);
+          } else {
+            tma_load_2d_pair(m_dst, &p.tmM, bar, j, t.row0 + r);
+            tma_load_2d_pair(m_dst + 8192, &p.tmM, bar, j + 64, t.row0 + r);
+          }
+          if (N_MN) {
+            for (int x = 0; x < n_boxes; ++x)
+              tma_load_2d_pair(n_dst + x * 8192, &p.tmN[0], bar, i + 64 * x, t.row0 + r);
+          } else {
+            // half (a multiple of 16) as boxes of 128, 64, 32 and 16 rows
+            int at = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int h = 128 >> x;
+              if (half & h) {
+                tma_load_2d_pair(n_dst + at * (BK * 2), &p.tmN[x], bar, r, t.row0 + i + at);
+                at += h;
+              }
+            }
+          }
+          used |= 1u << stage;
+          last = (last & ~(1u << stage)) | (phase << stage);
+          if (partial) used &= ~(1u << stage);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      pdl_trigger();
+      // Wait (bounded) until the last load issued on every stage has landed,
+      // so that no copy still writes shared memory when the block exits.
+      const uint64_t t0 = globaltimer_ns();
+      for (int s = 0; s < STAGES; ++s) {
+        const bool on_full = leader && ((used >> s) & 1u);
+        const bool on_tail = (tails >> s) & 1u;
+        while ((on_full && !mbar_try_wait(&full[s], (last >> s) & 1u)) ||
+               (on_tail && !mbar_try_wait(&tail[s], ((tail_par >> s) & 1u) ^ 1u))) {
+          if (globaltimer_ns() - t0 > kWaitLimitNs) { record_status(p.status, DEV_WAIT_TIMEOUT); break; }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------- MMA issuer (rank 0), partial blocks (both)
+    const uint32_t idesc_base = p.fmt | (1u << 4) | (M_MN ? 1u << 15 : 0u) | (N_MN ? 1u << 16 : 0u) |
+                                (static_cast<uint32_t>(TM >> 4) << 24);
+    int stage = 0;
+    uint32_t phase = 0, tail_par = 0;
+    int it = 0;                                            // chains so far
+    bool ok = true;
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+      const uint32_t idesc = idesc_base | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
+      for (int b = 0; b < t.blocks; ++b) {
+        const bool first = b % p.chain == 0, last_of_chain = (b + 1) % p.chain == 0 || b + 1 == t.blocks;
+        const int acc = it & 1;
+        const int valid = FORM == kWgrad ? min(BK, t.rows - b * BK) : BK;
+        if (leader) {
+          int got = 1;
+          if (lane == 0) {
+            if (first) got = mbar_wait_cluster(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, p.status) ? 1 : 0;
+            if (got) got = mbar_wait_cluster(&full[stage], phase, s_abort, p.status) ? 1 : 0;
+          }
+          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+          if (!ok) break;
+        }
+        uint8_t* m_src = smem + stage * STAGE_BYTES;
+        if (FORM == kWgrad && valid < BK) {
+          // this CTA's loads have landed; zero the rows past the group up to
+          // the next multiple of 16
+          int got = 1;
+          if (lane == 0) got = mbar_wait(&tail[stage], (tail_par >> stage) & 1u, s_abort, p.status) ? 1 : 0;
+          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+          if (!ok) break;
+          tail_par ^= 1u << stage;
+          const int count = (((valid + 15) & ~15) - valid) * 8;     // 16-byte pieces a box
+          const int boxes = 2 + (((t.mma_n >> 1) + 63) >> 6);       // M side, then N side
+          for (int x = lane; x < boxes * count; x += 32) {
+            const int box = x / count;
+            *reinterpret_cast<uint4*>(m_src + (box < 2 ? box * 8192 : SIDE_BYTES + (box - 2) * 8192) +
+                                      valid * 128 + (x - box * count) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (!leader && lane == 0) mbar_arrive_cluster(mapa_shared(&full[stage], 0));
+        }
+        if (leader && lane == 0) {
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TN);
+          const uint32_t ma = smem_u32(m_src), na = ma + SIDE_BYTES;
+          const uint64_t mdesc = M_MN ? smem_desc_mnmajor_sw128(ma) : smem_desc_kmajor_sw128(ma);
+          const uint64_t ndesc = N_MN ? smem_desc_mnmajor_sw128(na) : smem_desc_kmajor_sw128(na);
+          // one K=16 step: 32 bytes along a K-major row, 16 rows of an MN-major box
+          constexpr uint64_t m_step = M_MN ? 2048 >> 4 : 32 >> 4, n_step = N_MN ? 2048 >> 4 : 32 >> 4;
+          const int steps = FORM == kWgrad ? (valid + 15) >> 4 : BK / 16;
+          for (int s = 0; s < steps; ++s)
+            mma_bf16_ss_pair(d_tmem, mdesc + s * m_step, ndesc + s * n_step, idesc, !first || s > 0 ? 1u : 0u);
+          mma_commit_pair(&empty[stage], 0x3);             // frees the stage in both CTAs
+          if (last_of_chain) mma_commit_pair(&tfull[acc], 0x3);
+        }
+        if (last_of_chain) ++it;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (leader && lane == 0) {
+      // every MMA issued must be complete before tensor memory is freed
+      mma_commit_pair(drain, 0x1);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) { record_status(p.status, DEV_WAIT_TIMEOUT); break; }
+      }
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    int it = 0;
+    bool ok = true;
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+      const int j = t.j0 + rank * 128 + quarter * 32 + lane;
+      const int64_t first_row = FORM == kWgrad ? static_cast<int64_t>(t.e) * p.n_i + t.i0
+                                               : static_cast<int64_t>(t.row0) + t.i0;
+      const int64_t at = first_row * p.n_j + j;
+      const bool live = j < p.n_j;
+      if (t.blocks == 0) {                                 // wgrad of an expert without rows
+        if (live) {
+          for (int i = 0; i < t.ni; ++i) {
+            if (p.out_f32) static_cast<float*>(p.out)[at + static_cast<int64_t>(i) * p.n_j] = 0.0f;
+            else static_cast<uint16_t*>(p.out)[at + static_cast<int64_t>(i) * p.n_j] = 0;
+          }
+        }
+        continue;
+      }
+      for (int b = 0; b < t.blocks; b += p.chain, ++it) {
+        const int acc = it & 1;
+        if (!mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
+        tc_fence_after();
+        const bool add = b > 0 || p.accumulate;
+#pragma unroll 1
+        for (int c = 0; c < t.ni; c += 32) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
+          tmem_ld_wait();
+          const int left = live ? t.ni - c : 0;            // rows of this lane's column to store
+          if (p.out_f32) {
+            float* o = static_cast<float*>(p.out) + at + static_cast<int64_t>(c) * p.n_j;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < left) {
+                float* d = o + static_cast<int64_t>(i) * p.n_j;
+                const float x = __uint_as_float(v[i]);
+                *d = add ? *d + x : x;
+              }
+          } else {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + at + static_cast<int64_t>(c) * p.n_j;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < left) {
+                const float x = __uint_as_float(v[i]);
+                o[static_cast<int64_t>(i) * p.n_j] =
+                    p.out_f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+              }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));   // the issuer's barrier
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                        // no MMA or signal of the pair is still in flight
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// ----------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// 16-bit tensor of `depth` matrices [rows, cols] (depth 0: one, as a 2-D
+// map), boxes of 64 columns x box_rows, 128-byte swizzle.
+bool encode(CUtensorMap* m, const void* base, int f16, int64_t cols, int64_t rows, int depth, int box_rows) {
+  auto fn = encoder();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(depth)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * 2 * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[3] = {BK, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int FORM>
+cudaError_t launch_form(const ProductParams& p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  const int smem = Smem::bytes(p.E);
+  static std::atomic<int> configured[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool cached = dev >= 0 && dev < 64;
+  if (!cached || configured[dev].load(std::memory_order_relaxed) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::bytes(1024));
+    if (e != cudaSuccess) return e;
+    if (cached) configured[dev].store(1, std::memory_order_relaxed);
+  }
+  int64_t units = num_sms / 2;
+  if (max_tiles < units) units = max_tiles > 0 ? max_tiles : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
+  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM>, p);
+}
+
+}  // namespace
+
+bool grouped_matmul_sm100_takes(const GroupedProduct& g) {
+  return g.dtype != MOE_ELEM_F32 && g.n % 8 == 0 && g.k % 8 == 0;
+}
+
+cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cudaStream_t stream,
+                                        bool* map_error) {
+  *map_error = false;
+  const int f16 = g.dtype == MOE_ELEM_F16;
+  ProductParams p{};
+  p.offsets = g.offsets;
+  p.status = g.status;
+  p.out = g.out;
+  p.E = g.E;
+  p.rows_cap = static_cast<int>(g.rows);
+  p.out_f32 = g.out_dtype == MOE_ELEM_F32;
+  p.out_f16 = g.out_dtype == MOE_ELEM_F16;
+  p.accumulate = g.accumulate;
+  p.fmt = f16 ? 0u : (1u << 7) | (1u << 10);
+  p.chain = p.out_f32 ? kChain : INT32_MAX;
+  const int64_t rows = g.rows > 0 ? g.rows : 1;   // wgrad of no rows: maps are never read
+  bool ok;
+  int64_t max_tiles;
+  if (g.form == kWgrad) {
+    p.n_i = g.n;
+    p.n_j = g.k;
+    const void* any = g.rows > 0 ? g.q : g.out;
+    ok = encode(&p.tmM, any, f16, g.k, rows, 0, BK) &&
+         encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, f16, g.n, rows, 0, BK);
+    p.tmN[1] = p.tmN[2] = p.tmN[3] = p.tmN[0];
+    max_tiles = static_cast<int64_t>(g.E) * tiles_over(g.n, TN) * tiles_over(g.k, TM);
+  } else {
+    const int red = g.form == kForward ? g.k : g.n;
+    p.n_j = g.form == kForward ? g.n : g.k;
+    p.n_r = red;
+    // forward: boxes of 64 k x 128 n; dgrad: 64 k x 64 n (k is j)
+    ok = encode(&p.tmM, g.q, f16, g.k, g.n, g.E, g.form == kForward ? 128 : BK);
+    for (int x = 0; x < 4; ++x) ok = ok && encode(&p.tmN[x], g.p, f16, red, rows, 0, 128 >> x);
+    max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
+  }
+  if (!ok) { *map_error = true; return cudaErrorInvalidValue; }
+  return g.form == kForward ? launch_form<kForward>(p, max_tiles, num_sms, stream)
+         : g.form == kDgrad ? launch_form<kDgrad>(p, max_tiles, num_sms, stream)
+                            : launch_form<kWgrad>(p, max_tiles, num_sms, stream);
+}
+
+}  // namespace moe

@@ -128,6 +128,11 @@ struct GroupedProduct {
 };
 // grouped_matmul_simt.cu (CUDA cores: fp32 operands, and sizes TMA cannot take)
 cudaError_t launch_grouped_matmul_simt(const GroupedProduct& g, int num_sms, cudaStream_t stream);
+// grouped_matmul_sm100.cu (tensor cores: 16-bit operands whose rows are whole
+// 16-byte vectors)
+bool grouped_matmul_sm100_takes(const GroupedProduct& g);
+cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cudaStream_t stream,
+                                        bool* map_error);
 
 // swiglu_checkpoint.cu
 struct SwigluArgs {

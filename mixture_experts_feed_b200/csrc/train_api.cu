@@ -59,7 +59,11 @@ moe_status_t run_grouped(const moe_grouped_desc_t* d, int form, const void* p, c
   g.out = out;
   g.accumulate = accumulate ? 1 : 0;
   g.status = static_cast<int32_t*>(ws);
-  return cuda_status(launch_grouped_matmul_simt(g, device_sm_count(), static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!grouped_matmul_sm100_takes(g)) return cuda_status(launch_grouped_matmul_simt(g, device_sm_count(), s));
+  bool map_error = false;
+  const cudaError_t e = launch_grouped_matmul_sm100(g, device_sm_count(), s, &map_error);
+  return map_error ? MOE_ERR_INVALID_ARG : cuda_status(e);
 }
 
 moe_status_t check_swiglu(int64_t rows, int32_t I, moe_dtype_t dtype, int32_t n_groups,
