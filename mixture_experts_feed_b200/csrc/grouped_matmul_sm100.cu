@@ -35,9 +35,11 @@
 // the chains of a tile are added in fp32 by the threads that store it, in
 // order.  16-bit outputs round away far more than that and take one chain.
 //
-// Roles (192 threads a CTA, one CTA an SM): warp 0 loads, warp 1 allocates
-// tensor memory and (rank 0) issues the MMAs, warps 2..5 store; two
-// accumulators let the stores of one tile overlap the MMAs of the next.
+// Roles (320 threads a CTA, one CTA an SM): warp 0 loads, warp 1 allocates
+// tensor memory and (rank 0) issues the MMAs, warps 2..9 store (through a
+// 2 KB staging box and TMA stores; accumulation into fp32 weight gradients is
+// TMA's add); two accumulators let the stores of one tile overlap the MMAs of
+// the next.
 // Every wait is bounded.
 #include <atomic>
 
@@ -60,31 +62,37 @@ constexpr int BK = 64;                   // r per stage
 constexpr int SIDE_BYTES = 128 * BK * 2; // one operand of a stage in one CTA
 constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
 constexpr int STAGES = 6;
-constexpr int NUM_THREADS = 192;
+constexpr int EPI_WARPS = 8;              // two per quarter of the tensor memory's lanes
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int OUT_BYTES = 2048;          // staging buffer: 32 j x 32 i (16-bit) or x 16 i (fp32)
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
 constexpr int kBand = 8;                 // i tiles per band (tile order)
-constexpr int kChain = 16;               // blocks of 64 per accumulation chain, fp32 outputs
+constexpr int kChain = 8;                // blocks of 64 per accumulation chain, fp32 outputs
+constexpr int kMaxSmem = 232448;         // shared memory a block can have
 
 struct alignas(64) ProductParams {
   CUtensorMap tmM;       // M side
   CUtensorMap tmN[4];    // N side: boxes of 128, 64, 32 and 16 rows (wgrad: [0] alone)
+  CUtensorMap tmOut;     // output [depth][i][j]: boxes of one staging buffer
   const int32_t* offsets;
   int32_t* status;
   void* out;
   int E, rows_cap;
   int n_i, n_j, n_r;     // sizes of i, j, r (0 where it is the group's rows)
-  int out_f32, out_f16, accumulate;
+  int out_f16, accumulate;
   uint32_t fmt;          // operand format bits of the MMA descriptor
-  int chain;             // blocks per accumulation chain
+  int out_bufs;          // staging buffers of an epilogue warp: 2, or 1 beside large tables
 };
 
 struct Smem {
-  static constexpr int kBars = STAGES * STAGE_BYTES;
+  static constexpr int kOut = STAGES * STAGE_BYTES;       // staging, out_bufs * 2 KB a warp
   // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain
   static constexpr int kNumBars = 3 * STAGES + 5;
-  static constexpr int kMisc = kBars + kNumBars * 8;      // tmem base, abort, bad
-  static constexpr int kTables = kMisc + 16;              // s_off[E + 1], s_tile[E + 1]
-  static int bytes(int E) { return 1024 + kTables + 8 * (E + 1); }
+  // behind it: the barriers, then tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
+  static constexpr int kFixed = kNumBars * 8 + 16;
+  static int bytes(int E, int bufs) {
+    return 1024 + kOut + bufs * EPI_WARPS * OUT_BYTES + kFixed + 8 * (E + 1);
+  }
 };
 
 __host__ __device__ __forceinline__ int tiles_over(int n, int t) { return (n + t - 1) / t; }
@@ -209,28 +217,114 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t smem_addr) 
   return d;
 }
 
+// One epilogue warp's staging buffers, used in turn; every use ends in one
+// bulk group (an empty one when the rows were stored by the threads).
+struct OutStage {
+  uint8_t* base;
+  int bufs, at;
+  // the next buffer, once the store that used it last has read it
+  __device__ __forceinline__ uint8_t* take(int lane) {
+    if (lane == 0) {
+      if (bufs == 2) bulk_wait_group_read1();
+      else bulk_wait_group_read0();
+    }
+    __syncwarp();
+    uint8_t* b = base + at * OUT_BYTES;
+    at = bufs == 2 ? at ^ 1 : 0;
+    return b;
+  }
+};
+
+// The box in `buf` ([rows][32 j]) to out rows row.. at column j.  Whole boxes
+// go by TMA, which clips at the edges of the output matrix (wgrad: of the
+// expert's matrix); a group's last rows are stored by the threads, since a
+// box would write the next group's rows.
+template <int FORM, int ELEM, int ROWS>
+__device__ __forceinline__ void store_box(const ProductParams& p, uint8_t* buf, int j, int row, int depth,
+                                          int left, int lane) {
+  if (FORM == kWgrad || left >= ROWS) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (FORM == kWgrad && ELEM == 4 && p.accumulate) tma_add_3d(&p.tmOut, buf, j, row, depth);
+      else tma_store_3d(&p.tmOut, buf, j, row, depth);
+      bulk_commit_group();
+    }
+  } else {
+    __syncwarp();
+    constexpr int PIECES = 32 * ELEM / 16;                 // 16-byte pieces a row
+#pragma unroll
+    for (int x = lane; x < ROWS * PIECES; x += 32) {
+      const int r = x / PIECES, jj = j + (x % PIECES) * (16 / ELEM);
+      if (r < left && jj < p.n_j)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
+                                  (static_cast<int64_t>(row + r) * p.n_j + jj) * ELEM) =
+            *reinterpret_cast<const uint4*>(buf + x * 16);
+    }
+    if (lane == 0) bulk_commit_group();
+    __syncwarp();
+  }
+}
+
+// 16 fp32 output rows, lane = j
+template <int FORM>
+__device__ __forceinline__ void store_f32(OutStage& os, const ProductParams& p, const float* v, int j,
+                                          int row, int depth, int left, int lane) {
+  uint8_t* buf = os.take(lane);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) *reinterpret_cast<float*>(buf + i * 128 + lane * 4) = v[i];
+  store_box<FORM, 4, 16>(p, buf, j, row, depth, left, lane);
+}
+
+// 32 16-bit output rows, lane = j: neighbouring lanes swap one value of each
+// pair of rows, so that each holds two neighbouring j of one row and a warp's
+// store covers two whole 64-byte rows of the box.
+template <int FORM>
+__device__ __forceinline__ void store_16(OutStage& os, const ProductParams& p, const uint32_t (&v)[32], int j,
+                                         int row, int depth, int left, int lane) {
+  uint8_t* buf = os.take(lane);
+  const bool odd = lane & 1;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t give = odd ? v[2 * i] : v[2 * i + 1];
+    const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 1));
+    const float lo = odd ? got : __uint_as_float(v[2 * i]), hi = odd ? __uint_as_float(v[2 * i + 1]) : got;
+    uint32_t w;
+    if (p.out_f16) {
+      const __half2 h = __floats2half2_rn(lo, hi);
+      w = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w = pack_bf16x2(lo, hi);
+    }
+    *reinterpret_cast<uint32_t*>(buf + (2 * i + (odd ? 1 : 0)) * 64 + (lane >> 1) * 4) = w;
+  }
+  store_box<FORM, 2, 32>(p, buf, j, row, depth, left, lane);
+}
+
 template <int FORM> struct Majors {
   static constexpr bool M_MN = FORM != kForward;   // M side MN-major (j contiguous)
   static constexpr bool N_MN = FORM == kWgrad;     // N side MN-major (i contiguous)
 };
 
-template <int FORM>
+template <int FORM, bool F32>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     grouped_matmul_kernel(const __grid_constant__ ProductParams p) {
   constexpr bool M_MN = Majors<FORM>::M_MN, N_MN = Majors<FORM>::N_MN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kBars);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kOut + p.out_bufs * EPI_WARPS * OUT_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tail = empty + STAGES;       // wgrad: a partial block's loads of this CTA
   uint64_t* tfull = tail + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Smem::kMisc);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + Smem::kMisc + 4);
-  int* s_bad = reinterpret_cast<int*>(smem + Smem::kMisc + 8);
-  int* s_off = reinterpret_cast<int*>(smem + Smem::kTables);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + Smem::kNumBars);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
+  int* s_off = reinterpret_cast<int*>(s_tmem + 4);
+  // blocks of 64 r that one accumulation chain takes
+  constexpr int kRun = F32 ? kChain : (1 << 30);
   int* s_tile = s_off + (p.E + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -249,7 +343,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&tfull[i], 1);
-        mbar_init(&tempty[i], 8);        // the epilogue warps of both CTAs
+        mbar_init(&tempty[i], 2 * EPI_WARPS);   // the epilogue warps of both CTAs
       }
       mbar_init(drain, 1);
       *s_abort = 0;
@@ -364,9 +458,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
       const uint32_t idesc = idesc_base | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
       for (int b = 0; b < t.blocks; ++b) {
-        const bool first = b % p.chain == 0, last_of_chain = (b + 1) % p.chain == 0 || b + 1 == t.blocks;
+        const bool first = b % kRun == 0, last_of_chain = (b + 1) % kRun == 0 || b + 1 == t.blocks;
         const int acc = it & 1;
-        const int valid = FORM == kWgrad ? min(BK, t.rows - b * BK) : BK;
         if (leader) {
           int got = 1;
           if (lane == 0) {
@@ -377,7 +470,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
         }
         uint8_t* m_src = smem + stage * STAGE_BYTES;
-        if (FORM == kWgrad && valid < BK) {
+        int steps = BK / 16;
+        if (FORM == kWgrad && b + 1 == t.blocks && t.rows < t.blocks * BK) {
+          const int valid = t.rows - b * BK;
+          steps = (valid + 15) >> 4;
           // this CTA's loads have landed; zero the rows past the group up to
           // the next multiple of 16
           int got = 1;
@@ -385,13 +481,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = __shfl_sync(0xffffffffu, got, 0) != 0;
           if (!ok) break;
           tail_par ^= 1u << stage;
-          const int count = (((valid + 15) & ~15) - valid) * 8;     // 16-byte pieces a box
-          const int boxes = 2 + (((t.mma_n >> 1) + 63) >> 6);       // M side, then N side
-          for (int x = lane; x < boxes * count; x += 32) {
-            const int box = x / count;
-            *reinterpret_cast<uint4*>(m_src + (box < 2 ? box * 8192 : SIDE_BYTES + (box - 2) * 8192) +
-                                      valid * 128 + (x - box * count) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          const int count = (16 * steps - valid) * 8;               // 16-byte pieces a box
+          const int boxes = 2 + (((t.mma_n >> 1) + 63) >> 6);
+          for (int box = 0; box < boxes; ++box)                     // M side's two, then N side's
+            for (int x = lane; x < count; x += 32)
+              *reinterpret_cast<uint4*>(m_src + box * 8192 + valid * 128 + x * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
           if (!leader && lane == 0) mbar_arrive_cluster(mapa_shared(&full[stage], 0));
@@ -404,7 +498,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint64_t ndesc = N_MN ? smem_desc_mnmajor_sw128(na) : smem_desc_kmajor_sw128(na);
           // one K=16 step: 32 bytes along a K-major row, 16 rows of an MN-major box
           constexpr uint64_t m_step = M_MN ? 2048 >> 4 : 32 >> 4, n_step = N_MN ? 2048 >> 4 : 32 >> 4;
-          const int steps = FORM == kWgrad ? (valid + 15) >> 4 : BK / 16;
           for (int s = 0; s < steps; ++s)
             mma_bf16_ss_pair(d_tmem, mdesc + s * m_step, ndesc + s * n_step, idesc, !first || s > 0 ? 1u : 0u);
           mma_commit_pair(&empty[stage], 0x3);             // frees the stage in both CTAs
@@ -425,63 +518,84 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
-    const int quarter = warp & 3;
+    // Warp w stores the lanes of quarter w % 4 (32 j) and every other chunk
+    // of 32 columns (i).
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    OutStage os{smem + Smem::kOut + (warp - 2) * p.out_bufs * OUT_BYTES, p.out_bufs, 0};
     int it = 0;
     bool ok = true;
     for (int tile = unit; tile < total && ok; tile += units) {
       const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
-      const int j = t.j0 + rank * 128 + quarter * 32 + lane;
-      const int64_t first_row = FORM == kWgrad ? static_cast<int64_t>(t.e) * p.n_i + t.i0
-                                               : static_cast<int64_t>(t.row0) + t.i0;
-      const int64_t at = first_row * p.n_j + j;
-      const bool live = j < p.n_j;
-      if (t.blocks == 0) {                                 // wgrad of an expert without rows
-        if (live) {
-          for (int i = 0; i < t.ni; ++i) {
-            if (p.out_f32) static_cast<float*>(p.out)[at + static_cast<int64_t>(i) * p.n_j] = 0.0f;
-            else static_cast<uint16_t*>(p.out)[at + static_cast<int64_t>(i) * p.n_j] = 0;
-          }
-        }
-        continue;
-      }
-      for (int b = 0; b < t.blocks; b += p.chain, ++it) {
-        const int acc = it & 1;
-        if (!mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
-        tc_fence_after();
-        const bool add = b > 0 || p.accumulate;
-#pragma unroll 1
-        for (int c = 0; c < t.ni; c += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
-          tmem_ld_wait();
-          const int left = live ? t.ni - c : 0;            // rows of this lane's column to store
-          if (p.out_f32) {
-            float* o = static_cast<float*>(p.out) + at + static_cast<int64_t>(c) * p.n_j;
+      const int j = t.j0 + rank * 128 + quarter * 32;
+      const int row = FORM == kWgrad ? t.i0 : t.row0 + t.i0;   // output row of column 0
+      const int depth = FORM == kWgrad ? t.e : 0;
+      if (F32) {
+        // the tile's chains added in registers, in order
+        float sum[4][32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < left) {
-                float* d = o + static_cast<int64_t>(i) * p.n_j;
-                const float x = __uint_as_float(v[i]);
-                *d = add ? *d + x : x;
-              }
-          } else {
-            uint16_t* o = static_cast<uint16_t*>(p.out) + at + static_cast<int64_t>(c) * p.n_j;
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < left) {
-                const float x = __uint_as_float(v[i]);
-                o[static_cast<int64_t>(i) * p.n_j] =
-                    p.out_f16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
-              }
+          for (int i = 0; i < 32; ++i) sum[x][i] = 0.0f;   // also what an expert without rows gets
+        for (int b = 0; b < t.blocks; b += kRun, ++it) {
+          const int acc = it & 1;
+          if (!mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int c = (2 * x + part) * 32;
+            if (c < t.ni) {                                // warp-uniform
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[x][i] += __uint_as_float(v[i]);
+            }
           }
+          tc_fence_before();
           __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));   // the issuer's barrier
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));   // the issuer's barrier
+        if (!ok) break;
+        if (j < p.n_j) {                                   // warp-uniform
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int c = (2 * x + part) * 32;
+            if (c < t.ni) {
+              store_f32<FORM>(os, p, &sum[x][0], j, row + c, depth, t.ni - c, lane);
+              if (c + 16 < t.ni) store_f32<FORM>(os, p, &sum[x][16], j, row + c + 16, depth, t.ni - c - 16, lane);
+            }
+          }
+        }
+      } else {
+        const int acc = it & 1;
+        if (t.blocks > 0) {
+          if (!mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
+          tc_fence_after();
+        }
+#pragma unroll 1
+        for (int c = part * 32; c < t.ni; c += 64) {
+          uint32_t v[32];
+          if (t.blocks > 0) {
+            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          }
+          if (j < p.n_j) store_16<FORM>(os, p, v, j, row + c, depth, t.ni - c, lane);
+        }
+        if (t.blocks > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));
+          ++it;
+        }
       }
     }
+    // the warp's stores complete before the block (and its shared memory) goes
+    if (lane == 0) bulk_wait_group0();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -506,32 +620,40 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// 16-bit tensor of `depth` matrices [rows, cols] (depth 0: one, as a 2-D
-// map), boxes of 64 columns x box_rows, 128-byte swizzle.
-bool encode(CUtensorMap* m, const void* base, int f16, int64_t cols, int64_t rows, int depth, int box_rows) {
+// Tensor of `depth` matrices [rows, cols] (depth 0: one, as a 2-D map), boxes
+// of box_cols x box_rows; operands with the 128-byte swizzle (64 16-bit
+// columns), outputs without.
+bool encode(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t rows, int depth, int box_cols,
+            int box_rows, bool swizzle) {
   auto fn = encoder();
   if (fn == nullptr) return false;
+  const cuuint64_t size = elem == MOE_ELEM_F32 ? 4 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(depth)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(cols) * 2 * static_cast<cuuint64_t>(rows)};
-  cuuint32_t box[3] = {BK, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * size,
+                           static_cast<cuuint64_t>(cols) * size * static_cast<cuuint64_t>(rows)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth > 0 ? 3 : 2,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUtensorMapDataType type = elem == MOE_ELEM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : elem == MOE_ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(m, type, depth > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            swizzle ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FORM>
-cudaError_t launch_form(const ProductParams& p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
-  const int smem = Smem::bytes(p.E);
+template <int FORM, bool F32>
+cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  p.out_bufs = Smem::bytes(p.E, 2) <= kMaxSmem ? 2 : 1;
+  const int smem = Smem::bytes(p.E, p.out_bufs);
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || configured[dev].load(std::memory_order_relaxed) == 0) {
-    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::bytes(1024));
+    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM, F32>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     if (cached) configured[dev].store(1, std::memory_order_relaxed);
   }
@@ -551,7 +673,7 @@ cudaError_t launch_form(const ProductParams& p, int64_t max_tiles, int num_sms, 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM>, p);
+  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM, F32>, p);
 }
 
 }  // namespace
@@ -570,11 +692,10 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
   p.out = g.out;
   p.E = g.E;
   p.rows_cap = static_cast<int>(g.rows);
-  p.out_f32 = g.out_dtype == MOE_ELEM_F32;
+  const bool f32 = g.out_dtype == MOE_ELEM_F32;
   p.out_f16 = g.out_dtype == MOE_ELEM_F16;
   p.accumulate = g.accumulate;
   p.fmt = f16 ? 0u : (1u << 7) | (1u << 10);
-  p.chain = p.out_f32 ? kChain : INT32_MAX;
   const int64_t rows = g.rows > 0 ? g.rows : 1;   // wgrad of no rows: maps are never read
   bool ok;
   int64_t max_tiles;
@@ -582,8 +703,9 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     p.n_i = g.n;
     p.n_j = g.k;
     const void* any = g.rows > 0 ? g.q : g.out;
-    ok = encode(&p.tmM, any, f16, g.k, rows, 0, BK) &&
-         encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, f16, g.n, rows, 0, BK);
+    ok = encode(&p.tmM, any, g.dtype, g.k, rows, 0, BK, BK, true) &&
+         encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, g.dtype, g.n, rows, 0, BK, BK, true) &&
+         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, 32, f32 ? 16 : 32, false);
     p.tmN[1] = p.tmN[2] = p.tmN[3] = p.tmN[0];
     max_tiles = static_cast<int64_t>(g.E) * tiles_over(g.n, TN) * tiles_over(g.k, TM);
   } else {
@@ -591,14 +713,20 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     p.n_j = g.form == kForward ? g.n : g.k;
     p.n_r = red;
     // forward: boxes of 64 k x 128 n; dgrad: 64 k x 64 n (k is j)
-    ok = encode(&p.tmM, g.q, f16, g.k, g.n, g.E, g.form == kForward ? 128 : BK);
-    for (int x = 0; x < 4; ++x) ok = ok && encode(&p.tmN[x], g.p, f16, red, rows, 0, 128 >> x);
+    ok = encode(&p.tmM, g.q, g.dtype, g.k, g.n, g.E, BK, g.form == kForward ? 128 : BK, true) &&
+         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, f32 ? 16 : 32, false);
+    for (int x = 0; x < 4; ++x)
+      ok = ok && encode(&p.tmN[x], g.p, g.dtype, red, rows, 0, BK, 128 >> x, true);
     max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
   }
   if (!ok) { *map_error = true; return cudaErrorInvalidValue; }
-  return g.form == kForward ? launch_form<kForward>(p, max_tiles, num_sms, stream)
-         : g.form == kDgrad ? launch_form<kDgrad>(p, max_tiles, num_sms, stream)
-                            : launch_form<kWgrad>(p, max_tiles, num_sms, stream);
+  if (f32)
+    return g.form == kForward ? launch_form<kForward, true>(p, max_tiles, num_sms, stream)
+           : g.form == kDgrad ? launch_form<kDgrad, true>(p, max_tiles, num_sms, stream)
+                              : launch_form<kWgrad, true>(p, max_tiles, num_sms, stream);
+  return g.form == kForward ? launch_form<kForward, false>(p, max_tiles, num_sms, stream)
+         : g.form == kDgrad ? launch_form<kDgrad, false>(p, max_tiles, num_sms, stream)
+                            : launch_form<kWgrad, false>(p, max_tiles, num_sms, stream);
 }
 
 }  // namespace moe
