@@ -25,7 +25,7 @@
 //
 // wgrad sums over a group's rows, whose last block of 64 may run into the
 // next group's rows (or rows that belong to nobody, which may hold NaN).
-// That block's loads complete on a barrier of their own CTA; warp 1 of each
+// That block's loads complete on a barrier of their own CTA; a warp of each
 // CTA then overwrites the foreign rows up to the next multiple of 16 with
 // zeros in shared memory, for both operands, and the MMA runs that many
 // 16-row steps.
@@ -35,8 +35,9 @@
 // the chains of a tile are added in fp32 by the threads that store it, in
 // order.  16-bit outputs round away far more than that and take one chain.
 //
-// Roles (320 threads a CTA, one CTA an SM): warp 0 loads, warp 1 allocates
-// tensor memory and (rank 0) issues the MMAs, warps 2..9 store (through a
+// Roles (352 threads a CTA, one CTA an SM): warp 0 loads, warp 1 allocates
+// tensor memory and (rank 0) issues the MMAs, warp 10 mends wgrad's partial
+// blocks, warps 2..9 store (through a
 // 2 KB staging box and TMA stores; accumulation into fp32 weight gradients is
 // TMA's add); two accumulators let the stores of one tile overlap the MMAs of
 // the next.
@@ -63,7 +64,8 @@ constexpr int SIDE_BYTES = 128 * BK * 2; // one operand of a stage in one CTA
 constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
 constexpr int STAGES = 6;
 constexpr int EPI_WARPS = 8;              // two per quarter of the tensor memory's lanes
-constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
+constexpr int FIX_WARP = 2 + EPI_WARPS;  // wgrad's last blocks
+constexpr int NUM_THREADS = 32 * (FIX_WARP + 1);
 constexpr int OUT_BYTES = 2048;          // staging buffer: 32 j x 32 i (16-bit) or x 16 i (fp32)
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
 constexpr int kBand = 8;                 // i tiles per band (tile order)
@@ -217,6 +219,36 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t smem_addr) 
   return d;
 }
 
+// mbar_wait for a whole warp that can be late: one lane asks, and sleeps in
+// between, so that waiting warps leave the issue slots and the shared-memory
+// pipe to the warps that load and issue MMAs.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int32_t* status) {
+  int got = 1;
+  if ((threadIdx.x & 31) == 0 && !mbar_try_wait(bar, parity)) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+      if (*abort) { got = 0; break; }
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        record_status(status, DEV_WAIT_TIMEOUT);
+        *abort = 1;
+        got = 0;
+        break;
+      }
+      __nanosleep(100);
+    }
+  }
+  return __shfl_sync(0xffffffffu, got, 0) != 0;
+}
+
+// mbar_wait by a whole warp that stays converged; `cluster`: with acquire at
+// cluster scope.
+__device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                         bool cluster = false) {
+  const bool got = cluster ? mbar_wait_cluster(bar, parity, abort, status) : mbar_wait(bar, parity, abort, status);
+  return __all_sync(0xffffffffu, got);
+}
+
 // One epilogue warp's staging buffers, used in turn; every use ends in one
 // bulk group (an empty one when the rows were stored by the threads).
 struct OutStage {
@@ -327,7 +359,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int kRun = F32 ? kChain : (1 << 30);
   int* s_tile = s_off + (p.E + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // warp-uniform
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const bool leader = rank == 0;
@@ -337,7 +369,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < STAGES; ++i) {
-        mbar_init(&full[i], 1);
+        // one arrival with the expected bytes and, for wgrad, a second one: a
+        // partial block has one from each CTA's FIX_WARP instead
+        mbar_init(&full[i], FORM == kWgrad ? 2 : 1);
         mbar_init(&empty[i], 1);
         mbar_init(&tail[i], 1);
       }
@@ -372,34 +406,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t used = 0, last = 0;               // stages loaded, parity of their last load
-      uint32_t tails = 0, tail_par = 0;          // the same for tail[]
-      bool ok = true;
-      for (int tile = unit; tile < total && ok; tile += units) {
-        const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
-        const int j = t.j0 + rank * 128;
-        const int half = t.mma_n >> 1;                     // i rows of this CTA
-        const int i = t.i0 + rank * half;
-        const int n_boxes = N_MN ? (half + 63) >> 6 : 0;
-        const uint32_t bytes = SIDE_BYTES + (N_MN ? n_boxes * 8192 : half * (BK * 2));
-        for (int b = 0; b < t.blocks; ++b) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) { ok = false; break; }
-          uint8_t* m_dst = smem + stage * STAGE_BYTES;
-          uint8_t* n_dst = m_dst + SIDE_BYTES;
-          const int r = b * BK;
-          // wgrad: a last block past the group's rows completes on this CTA's own barrier
-          const bool partial = FORM == kWgrad && r + BK > t.rows;
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t used = 0, last = 0;               // stages loaded, parity of their last load
+    uint32_t tails = 0, tail_par = 0;          // the same for tail[]
+    bool ok = true;
+    for (int tile = unit; tile < total && ok; tile += units) {
+      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+      const int j = t.j0 + rank * 128;
+      const int half = t.mma_n >> 1;                     // i rows of this CTA
+      const int i = t.i0 + rank * half;
+      const int n_boxes = N_MN ? (half + 63) >> 6 : 0;
+      const uint32_t bytes = SIDE_BYTES + (N_MN ? n_boxes * 8192 : half * (BK * 2));
+      for (int b = 0; b < t.blocks; ++b) {
+        if (!all_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) { ok = false; break; }
+        uint8_t* m_dst = smem + stage * STAGE_BYTES;
+        uint8_t* n_dst = m_dst + SIDE_BYTES;
+        const int r = b * BK;
+        // wgrad: a last block past the group's rows completes on this CTA's own barrier
+        const bool partial = FORM == kWgrad && r + BK > t.rows;
+        if (elect_one()) {
           uint32_t bar;
           if (partial) {
             mbar_arrive_expect_tx(&tail[stage], bytes);
             bar = mapa_shared(&tail[stage], static_cast<uint32_t>(rank));
-            tails |= 1u << stage;
-            tail_par ^= 1u << stage;                       // set = parity 0 completed last
           } else {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+            if (leader) {
+              mbar_arrive_expect_tx(&full[stage], 2 * bytes);
+              if (FORM == kWgrad) mbar_arrive(&full[stage]);
+            }
             bar = mapa_shared(&full[stage], 0);
           }
           if (!M_MN) {
@@ -426,15 +461,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               }
             }
           }
-          used |= 1u << stage;
-          last = (last & ~(1u << stage)) | (phase << stage);
-          if (partial) used &= ~(1u << stage);
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
+        __syncwarp();
+        used = partial ? used & ~(1u << stage) : used | 1u << stage;
+        last = (last & ~(1u << stage)) | (phase << stage);
+        if (partial) {
+          tails |= 1u << stage;
+          tail_par ^= 1u << stage;                       // set = parity 0 completed last
+        }
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      pdl_trigger();
-      // Wait (bounded) until the last load issued on every stage has landed,
-      // so that no copy still writes shared memory when the block exits.
+    }
+    pdl_trigger();
+    // Wait (bounded) until the last load issued on every stage has landed,
+    // so that no copy still writes shared memory when the block exits.
+    if (lane == 0) {
       const uint64_t t0 = globaltimer_ns();
       for (int s = 0; s < STAGES; ++s) {
         const bool on_full = leader && ((used >> s) & 1u);
@@ -447,76 +488,89 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------- MMA issuer (rank 0), partial blocks (both)
-    const uint32_t idesc_base = p.fmt | (1u << 4) | (M_MN ? 1u << 15 : 0u) | (N_MN ? 1u << 16 : 0u) |
-                                (static_cast<uint32_t>(TM >> 4) << 24);
-    int stage = 0;
-    uint32_t phase = 0, tail_par = 0;
-    int it = 0;                                            // chains so far
-    bool ok = true;
-    for (int tile = unit; tile < total && ok; tile += units) {
-      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
-      const uint32_t idesc = idesc_base | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
-      for (int b = 0; b < t.blocks; ++b) {
-        const bool first = b % kRun == 0, last_of_chain = (b + 1) % kRun == 0 || b + 1 == t.blocks;
-        const int acc = it & 1;
-        if (leader) {
-          int got = 1;
-          if (lane == 0) {
-            if (first) got = mbar_wait_cluster(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, p.status) ? 1 : 0;
-            if (got) got = mbar_wait_cluster(&full[stage], phase, s_abort, p.status) ? 1 : 0;
-          }
-          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-          if (!ok) break;
-        }
-        uint8_t* m_src = smem + stage * STAGE_BYTES;
-        int steps = BK / 16;
-        if (FORM == kWgrad && b + 1 == t.blocks && t.rows < t.blocks * BK) {
-          const int valid = t.rows - b * BK;
-          steps = (valid + 15) >> 4;
-          // this CTA's loads have landed; zero the rows past the group up to
-          // the next multiple of 16
-          int got = 1;
-          if (lane == 0) got = mbar_wait(&tail[stage], (tail_par >> stage) & 1u, s_abort, p.status) ? 1 : 0;
-          ok = __shfl_sync(0xffffffffu, got, 0) != 0;
-          if (!ok) break;
-          tail_par ^= 1u << stage;
-          const int count = (16 * steps - valid) * 8;               // 16-byte pieces a box
-          const int boxes = 2 + (((t.mma_n >> 1) + 63) >> 6);
-          for (int box = 0; box < boxes; ++box)                     // M side's two, then N side's
-            for (int x = lane; x < count; x += 32)
-              *reinterpret_cast<uint4*>(m_src + box * 8192 + valid * 128 + x * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (!leader && lane == 0) mbar_arrive_cluster(mapa_shared(&full[stage], 0));
-        }
-        if (leader && lane == 0) {
+    // ------------------------------------------------------ MMA issuer (rank 0)
+    if (leader) {
+      const uint32_t idesc_base = p.fmt | (1u << 4) | (M_MN ? 1u << 15 : 0u) | (N_MN ? 1u << 16 : 0u) |
+                                  (static_cast<uint32_t>(TM >> 4) << 24);
+      // one K=16 step: 32 bytes along a K-major row, 16 rows of an MN-major box
+      constexpr uint64_t m_step = M_MN ? 2048 >> 4 : 32 >> 4, n_step = N_MN ? 2048 >> 4 : 32 >> 4;
+      constexpr uint64_t next_stage = STAGE_BYTES >> 4;
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t mdesc0 = M_MN ? smem_desc_mnmajor_sw128(s0) : smem_desc_kmajor_sw128(s0);
+      const uint64_t ndesc0 = N_MN ? smem_desc_mnmajor_sw128(s0 + SIDE_BYTES) : smem_desc_kmajor_sw128(s0 + SIDE_BYTES);
+      int stage = 0;
+      uint32_t phase = 0;
+      int it = 0;                                          // chains so far
+      bool ok = true;
+      for (int tile = unit; tile < total && ok; tile += units) {
+        const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+        const uint32_t idesc = idesc_base | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
+        for (int b0 = 0; b0 < t.blocks && ok; b0 += kRun, ++it) {
+          const int acc = it & 1;
+          const int b1 = min(t.blocks, b0 + kRun);
+          if (!all_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TN);
-          const uint32_t ma = smem_u32(m_src), na = ma + SIDE_BYTES;
-          const uint64_t mdesc = M_MN ? smem_desc_mnmajor_sw128(ma) : smem_desc_kmajor_sw128(ma);
-          const uint64_t ndesc = N_MN ? smem_desc_mnmajor_sw128(na) : smem_desc_kmajor_sw128(na);
-          // one K=16 step: 32 bytes along a K-major row, 16 rows of an MN-major box
-          constexpr uint64_t m_step = M_MN ? 2048 >> 4 : 32 >> 4, n_step = N_MN ? 2048 >> 4 : 32 >> 4;
-          for (int s = 0; s < steps; ++s)
-            mma_bf16_ss_pair(d_tmem, mdesc + s * m_step, ndesc + s * n_step, idesc, !first || s > 0 ? 1u : 0u);
-          mma_commit_pair(&empty[stage], 0x3);             // frees the stage in both CTAs
-          if (last_of_chain) mma_commit_pair(&tfull[acc], 0x3);
+          for (int b = b0; b < b1; ++b) {
+            // wgrad's last block may have been mended by the CTAs' threads
+            const bool last = FORM == kWgrad && b + 1 == t.blocks;
+            if (!all_wait(&full[stage], phase, s_abort, p.status, last)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t mdesc = mdesc0 + stage * next_stage, ndesc = ndesc0 + stage * next_stage;
+            const int steps = last ? (t.rows - b * BK + 15) >> 4 : BK / 16;
+            if (elect_one()) {
+#pragma unroll
+              for (int s = 0; s < BK / 16; ++s)
+                if (FORM != kWgrad || s < steps)
+                  mma_bf16_ss_pair(d_tmem, mdesc + s * m_step, ndesc + s * n_step, idesc,
+                                   b > b0 || s > 0 ? 1u : 0u);
+              mma_commit_pair(&empty[stage], 0x3);         // frees the stage in both CTAs
+              if (b + 1 == b1) mma_commit_pair(&tfull[acc], 0x3);
+            }
+            __syncwarp();
+            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          }
         }
-        if (last_of_chain) ++it;
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-    }
-    if (leader && lane == 0) {
       // every MMA issued must be complete before tensor memory is freed
-      mma_commit_pair(drain, 0x1);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_try_wait(drain, 0)) {
-        if (globaltimer_ns() - t0 > kWaitLimitNs) { record_status(p.status, DEV_WAIT_TIMEOUT); break; }
+      if (elect_one()) {
+        mma_commit_pair(drain, 0x1);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0)) {
+          if (globaltimer_ns() - t0 > kWaitLimitNs) { record_status(p.status, DEV_WAIT_TIMEOUT); break; }
+        }
       }
     }
     __syncwarp();
-  } else {
+  } else if (FORM == kWgrad && warp == FIX_WARP) {
+    // -------------------------- wgrad: the partial last block of a group's rows
+    int stage = 0;
+    uint32_t tail_par = 0;
+    for (int tile = unit; tile < total; tile += units) {
+      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+      if (t.blocks == 0) continue;
+      stage = (stage + t.blocks - 1) % STAGES;             // the last block's stage
+      const int valid = t.rows - (t.blocks - 1) * BK;
+      if (valid < BK) {
+        // this CTA's loads have landed: zero the rows past the group up to
+        // the next multiple of 16, in both operands
+        int got = 1;
+        if (lane == 0) got = mbar_wait(&tail[stage], (tail_par >> stage) & 1u, s_abort, p.status) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, got, 0)) break;
+        tail_par ^= 1u << stage;
+        uint8_t* base = smem + stage * STAGE_BYTES + valid * 128;
+        const int count = (((valid + 15) & ~15) - valid) * 8;       // 16-byte pieces a box
+        const int boxes = 2 + (((t.mma_n >> 1) + 63) >> 6);
+        for (int box = 0; box < boxes; ++box)                       // M side's two, then N side's
+          for (int x = lane; x < count; x += 32)
+            *reinterpret_cast<uint4*>(base + box * 8192 + x * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(&full[stage], 0));
+      }
+      stage = (stage + 1) % STAGES;
+    }
+  } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // -------------------------------------------------------------- epilogue
     // Warp w stores the lanes of quarter w % 4 (32 j) and every other chunk
     // of 32 columns (i).
@@ -539,7 +593,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < 32; ++i) sum[x][i] = 0.0f;   // also what an expert without rows gets
         for (int b = 0; b < t.blocks; b += kRun, ++it) {
           const int acc = it & 1;
-          if (!mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
+          if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -570,7 +624,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       } else {
         const int acc = it & 1;
         if (t.blocks > 0) {
-          if (!mbar_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
+          if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
         }
 #pragma unroll 1
