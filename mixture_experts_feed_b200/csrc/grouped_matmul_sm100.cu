@@ -62,11 +62,11 @@ constexpr int TN = 256;                  // i per tile, at most
 constexpr int BK = 64;                   // r per stage
 constexpr int SIDE_BYTES = 128 * BK * 2; // one operand of a stage in one CTA
 constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
-constexpr int STAGES = 6;
+constexpr int STAGES = 6;                // or one fewer beside large tables (many experts)
 constexpr int EPI_WARPS = 8;              // two per quarter of the tensor memory's lanes
 constexpr int FIX_WARP = 2 + EPI_WARPS;  // wgrad's last blocks
 constexpr int NUM_THREADS = 32 * (FIX_WARP + 1);
-constexpr int OUT_BYTES = 2048;          // staging buffer: 32 j x 32 i (16-bit) or x 16 i (fp32)
+constexpr int OUT_BYTES = 4096;          // an epilogue warp's staging: 32 j x 64 i (16-bit) or x 32 i (fp32)
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
 constexpr int kBand = 8;                 // i tiles per band (tile order)
 constexpr int kChain = 8;                // blocks of 64 per accumulation chain, fp32 outputs
@@ -83,17 +83,16 @@ struct alignas(64) ProductParams {
   int n_i, n_j, n_r;     // sizes of i, j, r (0 where it is the group's rows)
   int out_f16, accumulate;
   uint32_t fmt;          // operand format bits of the MMA descriptor
-  int out_bufs;          // staging buffers of an epilogue warp: 2, or 1 beside large tables
+  int stages;            // pipeline stages
 };
 
 struct Smem {
-  static constexpr int kOut = STAGES * STAGE_BYTES;       // staging, out_bufs * 2 KB a warp
   // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain
   static constexpr int kNumBars = 3 * STAGES + 5;
-  // behind it: the barriers, then tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
+  // the stages, 4 KB of staging a warp, the barriers, then tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
   static constexpr int kFixed = kNumBars * 8 + 16;
-  static int bytes(int E, int bufs) {
-    return 1024 + kOut + bufs * EPI_WARPS * OUT_BYTES + kFixed + 8 * (E + 1);
+  static int bytes(int E, int stages) {
+    return 1024 + stages * STAGE_BYTES + EPI_WARPS * OUT_BYTES + kFixed + 8 * (E + 1);
   }
 };
 
@@ -249,88 +248,45 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, got);
 }
 
-// One epilogue warp's staging buffers, used in turn; every use ends in one
-// bulk group (an empty one when the rows were stored by the threads).
-struct OutStage {
-  uint8_t* base;
-  int bufs, at;
-  // the next buffer, once the store that used it last has read it
-  __device__ __forceinline__ uint8_t* take(int lane) {
-    if (lane == 0) {
-      if (bufs == 2) bulk_wait_group_read1();
-      else bulk_wait_group_read0();
-    }
-    __syncwarp();
-    uint8_t* b = base + at * OUT_BYTES;
-    at = bufs == 2 ? at ^ 1 : 0;
-    return b;
-  }
-};
+// An epilogue warp stages 4 KB at a time, as two boxes of 2 KB ([i][32 j]:
+// 16-bit 32 rows of 64 bytes, fp32 16 rows of 128), then hands each to TMA
+// (flush_box).  The buffer is free again once the stores have read it.
+__device__ __forceinline__ void stage_free(int lane) {
+  if (lane == 0) bulk_wait_group_read0();
+  __syncwarp();
+}
 
-// The box in `buf` ([rows][32 j]) to out rows row.. at column j.  Whole boxes
-// go by TMA, which clips at the edges of the output matrix (wgrad: of the
-// expert's matrix); a group's last rows are stored by the threads, since a
-// box would write the next group's rows.
-template <int FORM, int ELEM, int ROWS>
-__device__ __forceinline__ void store_box(const ProductParams& p, uint8_t* buf, int j, int row, int depth,
-                                          int left, int lane) {
+// Byte offset of 16-byte piece c of row r inside a box: 16-bit boxes carry
+// TMA's 64-byte swizzle, which spreads the 8 rows a transposing store writes
+// at once over all banks.
+template <int ELEM> __device__ __forceinline__ int box_piece(int r, int c) {
+  return ELEM == 4 ? r * 128 + c * 16 : r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
+}
+
+// The box at `buf` to out rows row.. at column j; `left` rows of it count.
+// Whole boxes go by TMA, which clips at the edges of the output matrix (wgrad:
+// of the expert's matrix); a group's last rows are stored by the threads,
+// since a box would write the next group's rows.  The caller has made the
+// staged values visible to TMA.
+template <int FORM, int ELEM>
+__device__ __forceinline__ void flush_box(const ProductParams& p, const uint8_t* buf, int j, int row,
+                                          int depth, int left, int lane) {
+  constexpr int ROWS = ELEM == 4 ? 16 : 32, PIECES = 32 * ELEM / 16;   // 16-byte pieces a row
   if (FORM == kWgrad || left >= ROWS) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
+    if (left > 0 && lane == 0) {
       if (FORM == kWgrad && ELEM == 4 && p.accumulate) tma_add_3d(&p.tmOut, buf, j, row, depth);
       else tma_store_3d(&p.tmOut, buf, j, row, depth);
-      bulk_commit_group();
     }
   } else {
-    __syncwarp();
-    constexpr int PIECES = 32 * ELEM / 16;                 // 16-byte pieces a row
-#pragma unroll
-    for (int x = lane; x < ROWS * PIECES; x += 32) {
-      const int r = x / PIECES, jj = j + (x % PIECES) * (16 / ELEM);
-      if (r < left && jj < p.n_j)
+#pragma unroll 1
+    for (int x = lane; x < left * PIECES; x += 32) {
+      const int r = x / PIECES, c = x % PIECES, jj = j + c * (16 / ELEM);
+      if (jj < p.n_j)
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
                                   (static_cast<int64_t>(row + r) * p.n_j + jj) * ELEM) =
-            *reinterpret_cast<const uint4*>(buf + x * 16);
+            *reinterpret_cast<const uint4*>(buf + box_piece<ELEM>(r, c));
     }
-    if (lane == 0) bulk_commit_group();
-    __syncwarp();
   }
-}
-
-// 16 fp32 output rows, lane = j
-template <int FORM>
-__device__ __forceinline__ void store_f32(OutStage& os, const ProductParams& p, const float* v, int j,
-                                          int row, int depth, int left, int lane) {
-  uint8_t* buf = os.take(lane);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) *reinterpret_cast<float*>(buf + i * 128 + lane * 4) = v[i];
-  store_box<FORM, 4, 16>(p, buf, j, row, depth, left, lane);
-}
-
-// 32 16-bit output rows, lane = j: neighbouring lanes swap one value of each
-// pair of rows, so that each holds two neighbouring j of one row and a warp's
-// store covers two whole 64-byte rows of the box.
-template <int FORM>
-__device__ __forceinline__ void store_16(OutStage& os, const ProductParams& p, const uint32_t (&v)[32], int j,
-                                         int row, int depth, int left, int lane) {
-  uint8_t* buf = os.take(lane);
-  const bool odd = lane & 1;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t give = odd ? v[2 * i] : v[2 * i + 1];
-    const float got = __uint_as_float(__shfl_xor_sync(0xffffffffu, give, 1));
-    const float lo = odd ? got : __uint_as_float(v[2 * i]), hi = odd ? __uint_as_float(v[2 * i + 1]) : got;
-    uint32_t w;
-    if (p.out_f16) {
-      const __half2 h = __floats2half2_rn(lo, hi);
-      w = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      w = pack_bf16x2(lo, hi);
-    }
-    *reinterpret_cast<uint32_t*>(buf + (2 * i + (odd ? 1 : 0)) * 64 + (lane >> 1) * 4) = w;
-  }
-  store_box<FORM, 2, 32>(p, buf, j, row, depth, left, lane);
 }
 
 template <int FORM> struct Majors {
@@ -345,7 +301,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Smem::kOut + p.out_bufs * EPI_WARPS * OUT_BYTES);
+  const int stages = p.stages;
+  uint8_t* ring_end = smem + stages * STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring_end + EPI_WARPS * OUT_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* tail = empty + STAGES;       // wgrad: a partial block's loads of this CTA
   uint64_t* tfull = tail + STAGES;
@@ -469,7 +427,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tails |= 1u << stage;
           tail_par ^= 1u << stage;                       // set = parity 0 completed last
         }
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
       }
     }
     pdl_trigger();
@@ -528,7 +486,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (b + 1 == b1) mma_commit_pair(&tfull[acc], 0x3);
             }
             __syncwarp();
-            if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
           }
         }
       }
@@ -549,7 +507,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int tile = unit; tile < total; tile += units) {
       const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
       if (t.blocks == 0) continue;
-      stage = (stage + t.blocks - 1) % STAGES;             // the last block's stage
+      stage = (stage + t.blocks - 1) % stages;             // the last block's stage
       const int valid = t.rows - (t.blocks - 1) * BK;
       if (valid < BK) {
         // this CTA's loads have landed: zero the rows past the group up to
@@ -568,15 +526,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(&full[stage], 0));
       }
-      stage = (stage + 1) % STAGES;
+      stage = (stage + 1) % stages;
     }
   } else if (warp >= 2 && warp < 2 + EPI_WARPS) {
     // -------------------------------------------------------------- epilogue
-    // Warp w stores the lanes of quarter w % 4 (32 j) and every other chunk
-    // of 32 columns (i).
+    // Warp w stores the lanes of quarter w % 4 (32 j) and every other run of
+    // 64 (fp32: 32) columns (i).
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    OutStage os{smem + Smem::kOut + (warp - 2) * p.out_bufs * OUT_BYTES, p.out_bufs, 0};
+    uint8_t* st = ring_end + (warp - 2) * OUT_BYTES;
+    // transposing stores: lane 8m + r gives row r of an 8-row group, piece m
+    const uint32_t st_addr = smem_u32(st) + static_cast<uint32_t>(box_piece<2>(lane & 7, lane >> 3));
     int it = 0;
     bool ok = true;
     for (int tile = unit; tile < total && ok; tile += units) {
@@ -616,28 +576,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int x = 0; x < 4; ++x) {
             const int c = (2 * x + part) * 32;
             if (c < t.ni) {
-              store_f32<FORM>(os, p, &sum[x][0], j, row + c, depth, t.ni - c, lane);
-              if (c + 16 < t.ni) store_f32<FORM>(os, p, &sum[x][16], j, row + c + 16, depth, t.ni - c - 16, lane);
+              stage_free(lane);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(st + i * 128 + lane * 4) = sum[x][i];
+              fence_proxy_async_smem();
+              __syncwarp();
+              flush_box<FORM, 4>(p, st, j, row + c, depth, t.ni - c, lane);
+              flush_box<FORM, 4>(p, st + 2048, j, row + c + 16, depth, t.ni - c - 16, lane);
+              if (lane == 0) bulk_commit_group();
             }
           }
         }
       } else {
+        // 64 columns at a time: 8 x 8 fragments, rounded in pairs and stored
+        // transposed
         const int acc = it & 1;
         if (t.blocks > 0) {
           if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
         }
 #pragma unroll 1
-        for (int c = part * 32; c < t.ni; c += 64) {
-          uint32_t v[32];
+        for (int c = part * 64; c < t.ni; c += 128) {
+          uint32_t v[64];                                  // [lane half][column half][16]
           if (t.blocks > 0) {
-            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
+            const uint32_t src = t_lane + static_cast<uint32_t>(acc * TN + c);
+            tmem_ld_16x256b_x4(src, v);
+            tmem_ld_16x256b_x4(src + (16u << 16), v + 32);
+            if (c + 32 < t.mma_n) {
+              tmem_ld_16x256b_x4(src + 32, v + 16);
+              tmem_ld_16x256b_x4(src + 32 + (16u << 16), v + 48);
+            }
             tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0;
+            for (int i = 0; i < 64; ++i) v[i] = 0;
           }
-          if (j < p.n_j) store_16<FORM>(os, p, v, j, row + c, depth, t.ni - c, lane);
+          if (j < p.n_j) {                                 // warp-uniform
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float lo = __uint_as_float(v[2 * i]), hi = __uint_as_float(v[2 * i + 1]);
+              if (p.out_f16) {
+                const __half2 h = __floats2half2_rn(lo, hi);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
+              } else {
+                w[i] = pack_bf16x2(lo, hi);
+              }
+            }
+            stage_free(lane);
+            // w[16 h16 + 8 half + 2 n + h8]: j 16 h16 + 8 h8 .., i 32 half + 8 n ..
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                stmatrix_x4_trans(st_addr + half * 2048 + n * 512, w[8 * half + 2 * n], w[8 * half + 2 * n + 1],
+                                  w[16 + 8 * half + 2 * n], w[16 + 8 * half + 2 * n + 1]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            flush_box<FORM, 2>(p, st, j, row + c, depth, t.ni - c, lane);
+            flush_box<FORM, 2>(p, st + 2048, j, row + c + 32, depth, t.ni - c - 32, lane);
+            if (lane == 0) bulk_commit_group();
+          }
         }
         if (t.blocks > 0) {
           tc_fence_before();
@@ -675,10 +674,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // Tensor of `depth` matrices [rows, cols] (depth 0: one, as a 2-D map), boxes
-// of box_cols x box_rows; operands with the 128-byte swizzle (64 16-bit
-// columns), outputs without.
+// of box_cols x box_rows, swizzled as told.
 bool encode(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t rows, int depth, int box_cols,
-            int box_rows, bool swizzle) {
+            int box_rows, CUtensorMapSwizzle swizzle) {
   auto fn = encoder();
   if (fn == nullptr) return false;
   const cuuint64_t size = elem == MOE_ELEM_F32 ? 4 : 2;
@@ -692,15 +690,15 @@ bool encode(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t ro
                                    : elem == MOE_ELEM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return fn(m, type, depth > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-            swizzle ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            swizzle == CU_TENSOR_MAP_SWIZZLE_128B ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int FORM, bool F32>
 cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
-  p.out_bufs = Smem::bytes(p.E, 2) <= kMaxSmem ? 2 : 1;
-  const int smem = Smem::bytes(p.E, p.out_bufs);
+  p.stages = Smem::bytes(p.E, STAGES) <= kMaxSmem ? STAGES : STAGES - 1;
+  const int smem = Smem::bytes(p.E, p.stages);
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
@@ -751,15 +749,17 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
   p.accumulate = g.accumulate;
   p.fmt = f16 ? 0u : (1u << 7) | (1u << 10);
   const int64_t rows = g.rows > 0 ? g.rows : 1;   // wgrad of no rows: maps are never read
+  const CUtensorMapSwizzle kIn = CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapSwizzle kOut = f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B;
   bool ok;
   int64_t max_tiles;
   if (g.form == kWgrad) {
     p.n_i = g.n;
     p.n_j = g.k;
     const void* any = g.rows > 0 ? g.q : g.out;
-    ok = encode(&p.tmM, any, g.dtype, g.k, rows, 0, BK, BK, true) &&
-         encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, g.dtype, g.n, rows, 0, BK, BK, true) &&
-         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, 32, f32 ? 16 : 32, false);
+    ok = encode(&p.tmM, any, g.dtype, g.k, rows, 0, BK, BK, kIn) &&
+         encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, g.dtype, g.n, rows, 0, BK, BK, kIn) &&
+         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, 32, f32 ? 16 : 32, kOut);
     p.tmN[1] = p.tmN[2] = p.tmN[3] = p.tmN[0];
     max_tiles = static_cast<int64_t>(g.E) * tiles_over(g.n, TN) * tiles_over(g.k, TM);
   } else {
@@ -767,10 +767,10 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     p.n_j = g.form == kForward ? g.n : g.k;
     p.n_r = red;
     // forward: boxes of 64 k x 128 n; dgrad: 64 k x 64 n (k is j)
-    ok = encode(&p.tmM, g.q, g.dtype, g.k, g.n, g.E, BK, g.form == kForward ? 128 : BK, true) &&
-         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, f32 ? 16 : 32, false);
+    ok = encode(&p.tmM, g.q, g.dtype, g.k, g.n, g.E, BK, g.form == kForward ? 128 : BK, kIn) &&
+         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, f32 ? 16 : 32, kOut);
     for (int x = 0; x < 4; ++x)
-      ok = ok && encode(&p.tmN[x], g.p, g.dtype, red, rows, 0, BK, 128 >> x, true);
+      ok = ok && encode(&p.tmN[x], g.p, g.dtype, red, rows, 0, BK, 128 >> x, kIn);
     max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
   }
   if (!ok) { *map_error = true; return cudaErrorInvalidValue; }
