@@ -35,12 +35,11 @@
 // the chains of a tile are added in fp32 by the threads that store it, in
 // order.  16-bit outputs round away far more than that and take one chain.
 //
-// Roles (352 threads a CTA, one CTA an SM): warp 0 loads, warp 1 allocates
-// tensor memory and (rank 0) issues the MMAs, warp 10 mends wgrad's partial
-// blocks, warps 2..9 store (through a
-// 2 KB staging box and TMA stores; accumulation into fp32 weight gradients is
-// TMA's add); two accumulators let the stores of one tile overlap the MMAs of
-// the next.
+// Roles (one CTA an SM): warp 0 loads, warp 1 allocates tensor memory and
+// (rank 0) issues the MMAs, warp 10 works the tiles out, warp 11 mends wgrad's
+// partial blocks, warps 2..9 store (through staging boxes and TMA stores;
+// accumulation into fp32 weight gradients is TMA's add); two accumulators let
+// the stores of one tile overlap the MMAs of the next.
 // Every wait is bounded.
 #include <atomic>
 
@@ -64,10 +63,12 @@ constexpr int SIDE_BYTES = 128 * BK * 2; // one operand of a stage in one CTA
 constexpr int STAGE_BYTES = 2 * SIDE_BYTES;
 constexpr int STAGES = 6;                // or one fewer beside large tables (many experts)
 constexpr int EPI_WARPS = 8;              // two per quarter of the tensor memory's lanes
-constexpr int FIX_WARP = 2 + EPI_WARPS;  // wgrad's last blocks
-constexpr int NUM_THREADS = 32 * (FIX_WARP + 1);
+constexpr int SCHED_WARP = 2 + EPI_WARPS;
+constexpr int FIX_WARP = SCHED_WARP + 1; // wgrad's last blocks
+__host__ __device__ constexpr int num_threads(int form) { return 32 * (form == kWgrad ? FIX_WARP + 1 : FIX_WARP); }
 constexpr int OUT_BYTES = 4096;          // an epilogue warp's staging: 32 j x 64 i (16-bit) or x 32 i (fp32)
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
+constexpr int TQ = 8;                    // slots of the tile queue
 constexpr int kBand = 8;                 // i tiles per band (tile order)
 constexpr int kChain = 8;                // blocks of 64 per accumulation chain, fp32 outputs
 constexpr int kMaxSmem = 232448;         // shared memory a block can have
@@ -81,16 +82,17 @@ struct alignas(64) ProductParams {
   void* out;
   int E, rows_cap;
   int n_i, n_j, n_r;     // sizes of i, j, r (0 where it is the group's rows)
-  int out_f16, accumulate;
+  int accumulate;
   uint32_t fmt;          // operand format bits of the MMA descriptor
   int stages;            // pipeline stages
 };
 
 struct Smem {
-  // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain
-  static constexpr int kNumBars = 3 * STAGES + 5;
-  // the stages, 4 KB of staging a warp, the barriers, then tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
-  static constexpr int kFixed = kNumBars * 8 + 16;
+  // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain, tq[TQ], tqe[TQ]
+  static constexpr int kNumBars = 3 * STAGES + 5 + 2 * TQ;
+  // the stages, 4 KB of staging a warp, the tile queue, the barriers, then
+  // tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
+  static constexpr int kFixed = TQ * 32 + kNumBars * 8 + 16;
   static int bytes(int E, int stages) {
     return 1024 + stages * STAGE_BYTES + EPI_WARPS * OUT_BYTES + kFixed + 8 * (E + 1);
   }
@@ -153,14 +155,14 @@ __device__ __forceinline__ void build_tables(const ProductParams& p, int* s_off,
   __syncwarp();
 }
 
-struct TileInfo {
+struct alignas(32) TileInfo {
   int e;         // group
   int row0;      // the group's first row
   int rows;      // its rows
   int i0, j0;    // tile origin (i inside the group for forward and dgrad)
   int ni;        // valid i in the tile
   int mma_n;     // N of its MMAs: ni rounded up to 32
-  int blocks;    // blocks of 64 r
+  int blocks;    // blocks of 64 r; -1: no more tiles
 };
 
 // Tile `tile` of the launch.  Inside a group the shorter tile side runs
@@ -251,8 +253,8 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatil
 // An epilogue warp stages 4 KB at a time, as two boxes of 2 KB ([i][32 j]:
 // 16-bit 32 rows of 64 bytes, fp32 16 rows of 128), then hands each to TMA
 // (flush_box).  The buffer is free again once the stores have read it.
-__device__ __forceinline__ void stage_free(int lane) {
-  if (lane == 0) bulk_wait_group_read0();
+__device__ __forceinline__ void stage_free() {
+  if (elect_one()) bulk_wait_group_read0();
   __syncwarp();
 }
 
@@ -273,7 +275,7 @@ __device__ __forceinline__ void flush_box(const ProductParams& p, const uint8_t*
                                           int depth, int left, int lane) {
   constexpr int ROWS = ELEM == 4 ? 16 : 32, PIECES = 32 * ELEM / 16;   // 16-byte pieces a row
   if (FORM == kWgrad || left >= ROWS) {
-    if (left > 0 && lane == 0) {
+    if (left > 0 && elect_one()) {
       if (FORM == kWgrad && ELEM == 4 && p.accumulate) tma_add_3d(&p.tmOut, buf, j, row, depth);
       else tma_store_3d(&p.tmOut, buf, j, row, depth);
     }
@@ -294,21 +296,25 @@ template <int FORM> struct Majors {
   static constexpr bool N_MN = FORM == kWgrad;     // N side MN-major (i contiguous)
 };
 
-template <int FORM, bool F32>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+template <int FORM, int OUT>
+__global__ void __launch_bounds__(num_threads(FORM), 1)
     grouped_matmul_kernel(const __grid_constant__ ProductParams p) {
   constexpr bool M_MN = Majors<FORM>::M_MN, N_MN = Majors<FORM>::N_MN;
+  constexpr bool F32 = OUT == MOE_ELEM_F32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int stages = p.stages;
   uint8_t* ring_end = smem + stages * STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring_end + EPI_WARPS * OUT_BYTES);
+  TileInfo* s_tq = reinterpret_cast<TileInfo*>(ring_end + EPI_WARPS * OUT_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_tq + TQ);
   uint64_t* empty = full + STAGES;
   uint64_t* tail = empty + STAGES;       // wgrad: a partial block's loads of this CTA
   uint64_t* tfull = tail + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
+  uint64_t* tq = drain + 1;              // a tile is in the queue; its readers have it
+  uint64_t* tqe = tq + TQ;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + Smem::kNumBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
@@ -338,6 +344,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_init(&tempty[i], 2 * EPI_WARPS);   // the epilogue warps of both CTAs
       }
       mbar_init(drain, 1);
+      for (int i = 0; i < TQ; ++i) {
+        mbar_init(&tq[i], 1);
+        // the producer and the epilogue warps; rank 0's issuer; wgrad's FIX_WARP
+        mbar_init(&tqe[i], 1 + EPI_WARPS + (leader ? 1 : 0) + (FORM == kWgrad ? 1 : 0));
+      }
       *s_abort = 0;
       *s_bad = 0;
       fence_mbar_init();
@@ -362,6 +373,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int total = s_tile[p.E];
   if (threadIdx.x == 0 && *s_bad) record_status(p.status, DEV_BAD_ROW);
 
+  // The tile sequence of this pair: tiles unit, unit + units, ...  A warp of
+  // each CTA works them out ahead of the others (a search and a few divisions
+  // that would otherwise sit between two tiles' loads and MMAs) and queues
+  // them: tile seq in slot seq % TQ, tq[slot] completes when it is there,
+  // tqe[slot] when every reader has it.
+  auto take = [&](int seq, TileInfo& t) {
+    const int slot = seq % TQ;
+    if (!all_wait(&tq[slot], (seq / TQ) & 1, s_abort, p.status)) return false;
+    t = s_tq[slot];
+    __syncwarp();
+    if (elect_one()) mbar_arrive(&tqe[slot]);
+    return t.blocks >= 0;
+  };
+
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     int stage = 0;
@@ -369,13 +394,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t used = 0, last = 0;               // stages loaded, parity of their last load
     uint32_t tails = 0, tail_par = 0;          // the same for tail[]
     bool ok = true;
-    for (int tile = unit; tile < total && ok; tile += units) {
-      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+    TileInfo t;
+    for (int seq = 0; ok && take(seq, t); ++seq) {
       const int j = t.j0 + rank * 128;
       const int half = t.mma_n >> 1;                     // i rows of this CTA
       const int i = t.i0 + rank * half;
       const int n_boxes = N_MN ? (half + 63) >> 6 : 0;
       const uint32_t bytes = SIDE_BYTES + (N_MN ? n_boxes * 8192 : half * (BK * 2));
+      // an expert without rows (wgrad) passes one stage on without loads
+      if (FORM == kWgrad && t.blocks == 0) {
+        if (!all_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) break;
+        if (elect_one()) mbar_arrive_cluster(mapa_shared(&full[stage], 0));   // both CTAs: 2 arrivals
+        __syncwarp();
+        used &= ~(1u << stage);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
+        continue;
+      }
       for (int b = 0; b < t.blocks; ++b) {
         if (!all_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) { ok = false; break; }
         uint8_t* m_dst = smem + stage * STAGE_BYTES;
@@ -460,22 +494,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t phase = 0;
       int it = 0;                                          // chains so far
       bool ok = true;
-      for (int tile = unit; tile < total && ok; tile += units) {
-        const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+      TileInfo t;
+      for (int seq = 0; ok && take(seq, t); ++seq) {
+        t.blocks = __shfl_sync(0xffffffffu, t.blocks, 0);   // uniform registers again
+        t.rows = __shfl_sync(0xffffffffu, t.rows, 0);
+        t.mma_n = __shfl_sync(0xffffffffu, t.mma_n, 0);
         const uint32_t idesc = idesc_base | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
-        for (int b0 = 0; b0 < t.blocks && ok; b0 += kRun, ++it) {
+        // an expert without rows: one stage without MMAs
+        const int blocks = FORM == kWgrad ? max(t.blocks, 1) : t.blocks;
+        for (int b0 = 0; b0 < blocks && ok; b0 += kRun, ++it) {
           const int acc = it & 1;
-          const int b1 = min(t.blocks, b0 + kRun);
+          const int b1 = min(blocks, b0 + kRun);
           if (!all_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TN);
           for (int b = b0; b < b1; ++b) {
-            // wgrad's last block may have been mended by the CTAs' threads
-            const bool last = FORM == kWgrad && b + 1 == t.blocks;
-            if (!all_wait(&full[stage], phase, s_abort, p.status, last)) { ok = false; break; }
+            // a partial block (wgrad) has been mended by threads of both CTAs
+            const bool partial = FORM == kWgrad && (b + 1) * BK > t.rows;
+            if (!all_wait(&full[stage], phase, s_abort, p.status, partial)) { ok = false; break; }
             tc_fence_after();
             const uint64_t mdesc = mdesc0 + stage * next_stage, ndesc = ndesc0 + stage * next_stage;
-            const int steps = last ? (t.rows - b * BK + 15) >> 4 : BK / 16;
+            const int steps = partial ? (t.rows - b * BK + 15) >> 4 : BK / 16;
             if (elect_one()) {
 #pragma unroll
               for (int s = 0; s < BK / 16; ++s)
@@ -500,13 +539,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     __syncwarp();
+  } else if (warp == SCHED_WARP) {
+    // ------------------------------------------------------------- scheduler
+    for (int seq = 0;; ++seq) {
+      const int slot = seq % TQ;
+      const int64_t tile = unit + static_cast<int64_t>(seq) * units;
+      TileInfo t;
+      t.blocks = -1;
+      if (tile < total) t = tile_info<FORM>(static_cast<int>(tile), p, s_off, s_tile);
+      if (!all_wait(&tqe[slot], ((seq / TQ) & 1) ^ 1u, s_abort, p.status)) break;
+      if (elect_one()) {
+        s_tq[slot] = t;
+        mbar_arrive(&tq[slot]);
+      }
+      __syncwarp();
+      if (t.blocks < 0) break;
+    }
   } else if (FORM == kWgrad && warp == FIX_WARP) {
     // -------------------------- wgrad: the partial last block of a group's rows
     int stage = 0;
     uint32_t tail_par = 0;
-    for (int tile = unit; tile < total; tile += units) {
-      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
-      if (t.blocks == 0) continue;
+    TileInfo t;
+    for (int seq = 0; take(seq, t); ++seq) {
+      if (t.blocks == 0) {
+        stage = (stage + 1) % stages;
+        continue;
+      }
       stage = (stage + t.blocks - 1) % stages;             // the last block's stage
       const int valid = t.rows - (t.blocks - 1) * BK;
       if (valid < BK) {
@@ -539,8 +597,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t st_addr = smem_u32(st) + static_cast<uint32_t>(box_piece<2>(lane & 7, lane >> 3));
     int it = 0;
     bool ok = true;
-    for (int tile = unit; tile < total && ok; tile += units) {
-      const TileInfo t = tile_info<FORM>(tile, p, s_off, s_tile);
+    TileInfo t;
+    for (int seq = 0; ok && take(seq, t); ++seq) {
       const int j = t.j0 + rank * 128 + quarter * 32;
       const int row = FORM == kWgrad ? t.i0 : t.row0 + t.i0;   // output row of column 0
       const int depth = FORM == kWgrad ? t.e : 0;
@@ -551,14 +609,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[x][i] = 0.0f;   // also what an expert without rows gets
-        for (int b = 0; b < t.blocks; b += kRun, ++it) {
+        for (int b = 0; b < max(t.blocks, 1); b += kRun, ++it) {
           const int acc = it & 1;
           if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int c = (2 * x + part) * 32;
-            if (c < t.ni) {                                // warp-uniform
+            if (c < t.ni && t.blocks > 0) {                // warp-uniform
               uint32_t v[32];
               tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
               tmem_ld_wait();
@@ -576,14 +634,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int x = 0; x < 4; ++x) {
             const int c = (2 * x + part) * 32;
             if (c < t.ni) {
-              stage_free(lane);
+              stage_free();
 #pragma unroll
               for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(st + i * 128 + lane * 4) = sum[x][i];
               fence_proxy_async_smem();
               __syncwarp();
               flush_box<FORM, 4>(p, st, j, row + c, depth, t.ni - c, lane);
               flush_box<FORM, 4>(p, st + 2048, j, row + c + 16, depth, t.ni - c - 16, lane);
-              if (lane == 0) bulk_commit_group();
+              if (elect_one()) bulk_commit_group();
             }
           }
         }
@@ -591,10 +649,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // 64 columns at a time: 8 x 8 fragments, rounded in pairs and stored
         // transposed
         const int acc = it & 1;
-        if (t.blocks > 0) {
-          if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
-          tc_fence_after();
-        }
+        if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) break;
+        tc_fence_after();
+        auto release = [&] {                               // to the issuer's barrier
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));
+        };
 #pragma unroll 1
         for (int c = part * 64; c < t.ni; c += 128) {
           uint32_t v[64];                                  // [lane half][column half][16]
@@ -607,23 +668,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               tmem_ld_16x256b_x4(src + 32 + (16u << 16), v + 48);
             }
             tmem_ld_wait();
-          } else {
+          } else {                                         // wgrad of an expert without rows
 #pragma unroll
             for (int i = 0; i < 64; ++i) v[i] = 0;
           }
+          if (c + 128 >= t.ni) release();                  // this warp's last columns are in registers
           if (j < p.n_j) {                                 // warp-uniform
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float lo = __uint_as_float(v[2 * i]), hi = __uint_as_float(v[2 * i + 1]);
-              if (p.out_f16) {
+              if (OUT == MOE_ELEM_F16) {
                 const __half2 h = __floats2half2_rn(lo, hi);
                 w[i] = *reinterpret_cast<const uint32_t*>(&h);
               } else {
                 w[i] = pack_bf16x2(lo, hi);
               }
             }
-            stage_free(lane);
+            stage_free();
             // w[16 h16 + 8 half + 2 n + h8]: j 16 h16 + 8 h8 .., i 32 half + 8 n ..
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -635,19 +697,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             flush_box<FORM, 2>(p, st, j, row + c, depth, t.ni - c, lane);
             flush_box<FORM, 2>(p, st + 2048, j, row + c + 32, depth, t.ni - c - 32, lane);
-            if (lane == 0) bulk_commit_group();
+            if (elect_one()) bulk_commit_group();
           }
         }
-        if (t.blocks > 0) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));
-          ++it;
-        }
+        if (part * 64 >= t.ni) release();                  // no columns of its own
+        ++it;
       }
     }
     // the warp's stores complete before the block (and its shared memory) goes
-    if (lane == 0) bulk_wait_group0();
+    if (elect_one()) bulk_wait_group0();
     __syncwarp();
   }
 
@@ -695,7 +753,7 @@ bool encode(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t ro
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FORM, bool F32>
+template <int FORM, int OUT>
 cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
   p.stages = Smem::bytes(p.E, STAGES) <= kMaxSmem ? STAGES : STAGES - 1;
   const int smem = Smem::bytes(p.E, p.stages);
@@ -704,7 +762,7 @@ cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStr
   cudaGetDevice(&dev);
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || configured[dev].load(std::memory_order_relaxed) == 0) {
-    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM, F32>,
+    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM, OUT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     if (cached) configured[dev].store(1, std::memory_order_relaxed);
@@ -713,7 +771,7 @@ cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStr
   if (max_tiles < units) units = max_tiles > 0 ? max_tiles : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
-  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.blockDim = dim3(num_threads(FORM), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -725,7 +783,14 @@ cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStr
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM, F32>, p);
+  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM, OUT>, p);
+}
+
+template <int OUT>
+cudaError_t launch_out(int form, const ProductParams& p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
+  return form == kForward ? launch_form<kForward, OUT>(p, max_tiles, num_sms, stream)
+         : form == kDgrad ? launch_form<kDgrad, OUT>(p, max_tiles, num_sms, stream)
+                          : launch_form<kWgrad, OUT>(p, max_tiles, num_sms, stream);
 }
 
 }  // namespace
@@ -745,7 +810,6 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
   p.E = g.E;
   p.rows_cap = static_cast<int>(g.rows);
   const bool f32 = g.out_dtype == MOE_ELEM_F32;
-  p.out_f16 = g.out_dtype == MOE_ELEM_F16;
   p.accumulate = g.accumulate;
   p.fmt = f16 ? 0u : (1u << 7) | (1u << 10);
   const int64_t rows = g.rows > 0 ? g.rows : 1;   // wgrad of no rows: maps are never read
@@ -774,13 +838,9 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
   }
   if (!ok) { *map_error = true; return cudaErrorInvalidValue; }
-  if (f32)
-    return g.form == kForward ? launch_form<kForward, true>(p, max_tiles, num_sms, stream)
-           : g.form == kDgrad ? launch_form<kDgrad, true>(p, max_tiles, num_sms, stream)
-                              : launch_form<kWgrad, true>(p, max_tiles, num_sms, stream);
-  return g.form == kForward ? launch_form<kForward, false>(p, max_tiles, num_sms, stream)
-         : g.form == kDgrad ? launch_form<kDgrad, false>(p, max_tiles, num_sms, stream)
-                            : launch_form<kWgrad, false>(p, max_tiles, num_sms, stream);
+  return f32                              ? launch_out<MOE_ELEM_F32>(g.form, p, max_tiles, num_sms, stream)
+         : g.out_dtype == MOE_ELEM_F16    ? launch_out<MOE_ELEM_F16>(g.form, p, max_tiles, num_sms, stream)
+                                          : launch_out<MOE_ELEM_BF16>(g.form, p, max_tiles, num_sms, stream);
 }
 
 }  // namespace moe

@@ -102,6 +102,14 @@ def test_grouped_many_experts(form):
     check_grouped(form, sizes, 64, 72, BF, BF, pad=1)
 
 
+@pytest.mark.parametrize("form", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("sizes", [[300] + [0] * 300 + [40], [0] * 400, [0, 1] * 150],
+                         ids=["one", "none", "every other"])
+@pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
+def test_grouped_runs_of_experts_without_rows(form, sizes, out):
+    check_grouped(form, sizes, 520, 264, BF, out, pad=3)
+
+
 @pytest.mark.parametrize("form,n,k", [("forward", 256, 6144), ("dgrad", 6144, 256), ("wgrad", 256, 264)])
 def test_grouped_long_sums_in_fp32(form, n, k):
     """Long reductions with fp32 outputs: at most twice the error of fp32 sums
