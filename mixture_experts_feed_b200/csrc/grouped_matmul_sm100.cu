@@ -76,7 +76,8 @@ constexpr int kMaxSmem = 232448;         // shared memory a block can have
 struct alignas(64) ProductParams {
   CUtensorMap tmM;       // M side
   CUtensorMap tmN[4];    // N side: boxes of 128, 64, 32 and 16 rows (wgrad: [0] alone)
-  CUtensorMap tmOut;     // output [depth][i][j]: boxes of one staging buffer
+  CUtensorMap tmOut;     // output [depth][i][j]: boxes of 32 j x 64 i (16-bit) or 32 i (fp32)
+  CUtensorMap tmOut32;   // 16-bit: boxes of 32 j x 32 i
   const int32_t* offsets;
   int32_t* status;
   void* out;
@@ -250,38 +251,50 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, got);
 }
 
-// An epilogue warp stages 4 KB at a time, as two boxes of 2 KB ([i][32 j]:
-// 16-bit 32 rows of 64 bytes, fp32 16 rows of 128), then hands each to TMA
-// (flush_box).  The buffer is free again once the stores have read it.
+// An epilogue warp stages 4 KB at a time ([i][32 j]: 16-bit 64 rows of 64
+// bytes, fp32 32 rows of 128) and hands it to TMA (flush).  The buffer is free
+// again once the store has read it.
 __device__ __forceinline__ void stage_free() {
   if (elect_one()) bulk_wait_group_read0();
   __syncwarp();
 }
 
-// Byte offset of 16-byte piece c of row r inside a box: 16-bit boxes carry
+// Byte offset of 16-byte piece c of row r of the staging: 16-bit rows carry
 // TMA's 64-byte swizzle, which spreads the 8 rows a transposing store writes
 // at once over all banks.
 template <int ELEM> __device__ __forceinline__ int box_piece(int r, int c) {
   return ELEM == 4 ? r * 128 + c * 16 : r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
 }
 
-// The box at `buf` to out rows row.. at column j; `left` rows of it count.
-// Whole boxes go by TMA, which clips at the edges of the output matrix (wgrad:
-// of the expert's matrix); a group's last rows are stored by the threads,
-// since a box would write the next group's rows.  The caller has made the
-// staged values visible to TMA.
+// The staged rows to out rows row.. at column j; `left` of them count (a
+// multiple of 32 except at the end of i).  Whole boxes go by TMA, which clips
+// at the edges of the output matrix (wgrad: of the expert's matrix); a
+// group's last rows are stored by the threads, since a box would write the
+// next group's rows.
 template <int FORM, int ELEM>
-__device__ __forceinline__ void flush_box(const ProductParams& p, const uint8_t* buf, int j, int row,
-                                          int depth, int left, int lane) {
-  constexpr int ROWS = ELEM == 4 ? 16 : 32, PIECES = 32 * ELEM / 16;   // 16-byte pieces a row
-  if (FORM == kWgrad || left >= ROWS) {
-    if (left > 0 && elect_one()) {
+__device__ __forceinline__ void flush(const ProductParams& p, const uint8_t* buf, int j, int row, int depth,
+                                      int left, int lane) {
+  constexpr int ROWS = 128 / ELEM, PIECES = 32 * ELEM / 16;            // 16-byte pieces a row
+  fence_proxy_async_smem();
+  __syncwarp();
+  int done = 0;                                                        // rows that TMA takes
+  if (left >= ROWS || (FORM == kWgrad && left > ROWS - 32)) {
+    done = ROWS;
+    if (elect_one()) {
       if (FORM == kWgrad && ELEM == 4 && p.accumulate) tma_add_3d(&p.tmOut, buf, j, row, depth);
       else tma_store_3d(&p.tmOut, buf, j, row, depth);
+      bulk_commit_group();
     }
-  } else {
+  } else if (ELEM == 2 && (FORM == kWgrad || left >= 32)) {
+    done = 32;
+    if (elect_one()) {
+      tma_store_3d(&p.tmOut32, buf, j, row, depth);
+      bulk_commit_group();
+    }
+  }
+  if (FORM != kWgrad && done < left && done < ROWS) {
 #pragma unroll 1
-    for (int x = lane; x < left * PIECES; x += 32) {
+    for (int x = done * PIECES + lane; x < left * PIECES; x += 32) {
       const int r = x / PIECES, c = x % PIECES, jj = j + c * (16 / ELEM);
       if (jj < p.n_j)
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
@@ -289,6 +302,7 @@ __device__ __forceinline__ void flush_box(const ProductParams& p, const uint8_t*
             *reinterpret_cast<const uint4*>(buf + box_piece<ELEM>(r, c));
     }
   }
+  __syncwarp();
 }
 
 template <int FORM> struct Majors {
@@ -609,16 +623,18 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[x][i] = 0.0f;   // also what an expert without rows gets
-        for (int b = 0; b < max(t.blocks, 1); b += kRun, ++it) {
+        const int blocks = FORM == kWgrad ? max(t.blocks, 1) : t.blocks;
+        for (int b = 0; b < blocks; b += kRun, ++it) {
           const int acc = it & 1;
           if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
+          const uint32_t src = t_lane + static_cast<uint32_t>(acc * TN);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int c = (2 * x + part) * 32;
             if (c < t.ni && t.blocks > 0) {                // warp-uniform
               uint32_t v[32];
-              tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
+              tmem_ld_32x32b_x32(src + static_cast<uint32_t>(c), v);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 32; ++i) sum[x][i] += __uint_as_float(v[i]);
@@ -637,11 +653,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
               stage_free();
 #pragma unroll
               for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(st + i * 128 + lane * 4) = sum[x][i];
-              fence_proxy_async_smem();
-              __syncwarp();
-              flush_box<FORM, 4>(p, st, j, row + c, depth, t.ni - c, lane);
-              flush_box<FORM, 4>(p, st + 2048, j, row + c + 16, depth, t.ni - c - 16, lane);
-              if (elect_one()) bulk_commit_group();
+              flush<FORM, 4>(p, st, j, row + c, depth, t.ni - c, lane);
             }
           }
         }
@@ -693,11 +705,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
               for (int n = 0; n < 4; ++n)
                 stmatrix_x4_trans(st_addr + half * 2048 + n * 512, w[8 * half + 2 * n], w[8 * half + 2 * n + 1],
                                   w[16 + 8 * half + 2 * n], w[16 + 8 * half + 2 * n + 1]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            flush_box<FORM, 2>(p, st, j, row + c, depth, t.ni - c, lane);
-            flush_box<FORM, 2>(p, st + 2048, j, row + c + 32, depth, t.ni - c - 32, lane);
-            if (elect_one()) bulk_commit_group();
+            flush<FORM, 2>(p, st, j, row + c, depth, t.ni - c, lane);
           }
         }
         if (part * 64 >= t.ni) release();                  // no columns of its own
@@ -823,7 +831,8 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     const void* any = g.rows > 0 ? g.q : g.out;
     ok = encode(&p.tmM, any, g.dtype, g.k, rows, 0, BK, BK, kIn) &&
          encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, g.dtype, g.n, rows, 0, BK, BK, kIn) &&
-         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, 32, f32 ? 16 : 32, kOut);
+         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, 32, f32 ? 32 : 64, kOut) &&
+         encode(&p.tmOut32, g.out, g.out_dtype, g.k, g.n, g.E, 32, 32, kOut);
     p.tmN[1] = p.tmN[2] = p.tmN[3] = p.tmN[0];
     max_tiles = static_cast<int64_t>(g.E) * tiles_over(g.n, TN) * tiles_over(g.k, TM);
   } else {
@@ -832,7 +841,8 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     p.n_r = red;
     // forward: boxes of 64 k x 128 n; dgrad: 64 k x 64 n (k is j)
     ok = encode(&p.tmM, g.q, g.dtype, g.k, g.n, g.E, BK, g.form == kForward ? 128 : BK, kIn) &&
-         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, f32 ? 16 : 32, kOut);
+         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, f32 ? 32 : 64, kOut) &&
+         encode(&p.tmOut32, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, 32, kOut);
     for (int x = 0; x < 4; ++x)
       ok = ok && encode(&p.tmN[x], g.p, g.dtype, red, rows, 0, BK, 128 >> x, kIn);
     max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
