@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
       // an expert without rows (wgrad) passes one stage on without loads
       if (FORM == kWgrad && t.blocks == 0) {
         if (!all_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) break;
-        if (elect_one()) mbar_arrive_cluster(mapa_shared(&full[stage], 0));   // both CTAs: 2 arrivals
+        if (elect_one()) mbar_arrive_cluster_light(mapa_shared(&full[stage], 0));   // both CTAs: 2 arrivals
         __syncwarp();
         used &= ~(1u << stage);
         if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));   // the issuer's barrier
+          if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty[acc], 0));   // the issuer's barrier
         }
         if (!ok) break;
         if (j < p.n_j) {                                   // warp-uniform
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         auto release = [&] {                               // to the issuer's barrier
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[acc], 0));
+          if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty[acc], 0));
         };
 #pragma unroll 1
         for (int c = part * 64; c < t.ni; c += 128) {

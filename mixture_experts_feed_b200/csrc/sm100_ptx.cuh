@@ -258,6 +258,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same without the cluster-scope release, for signals that only order
+// tensor-memory accesses (tcgen05 fences do that): the release waits until
+// every earlier write of the thread is visible to the cluster (~2000 clocks
+// in a storing epilogue).
+__device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // try_wait with acquire at cluster scope: the waiter then sees what the
 // other CTA of the pair stored before its release-arrive on this barrier.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
