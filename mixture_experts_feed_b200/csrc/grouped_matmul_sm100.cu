@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
           for (int b = b0; b < b1; ++b) {
             // a partial block (wgrad) has been mended by threads of both CTAs
             const bool partial = FORM == kWgrad && (b + 1) * BK > t.rows;
-            if (!all_wait(&full[stage], phase, s_abort, p.status, partial)) { ok = false; break; }
+            if (!all_wait(&full[stage], phase, s_abort, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint64_t mdesc = mdesc0 + stage * next_stage, ndesc = ndesc0 + stage * next_stage;
             const int steps = partial ? (t.rows - b * BK + 15) >> 4 : BK / 16;
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
             *reinterpret_cast<uint4*>(base + box * 8192 + x * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(&full[stage], 0));
+        if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&full[stage], 0));
       }
       stage = (stage + 1) % stages;
     }
