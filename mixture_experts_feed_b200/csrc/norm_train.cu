@@ -16,10 +16,10 @@
 //
 // All passes are bound by HBM (backward: read x, dout and dres, write dx).
 // Rows of whole 16-byte vectors run in the *_rows kernels: a team of threads
-// holds a row in registers, 16 elements (8 to 32) a thread, so x and dout are
+// holds a row in registers, 8 to 32 elements a thread, so x and dout are
 // read once although the statistics need the whole row first.  Each thread
 // copies its own vectors of the rows to come into shared memory with cp.async,
-// one or two row groups ahead, and reads back only what it copied itself: the
+// two row groups ahead, and reads back only what it copied itself: the
 // loads stay in flight across the reductions with no barrier between them.
 // The reductions (RMSNorm one, layer norm two: the mean first) cost one block
 // barrier each, none when a team is one warp.  Other rows take the *_any
@@ -98,36 +98,71 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ------------------------------------------------------------- row teams
+// Two fp32 values a register pair: Blackwell's packed fp32 instructions do
+// both with one issue, and the issue rate is what bf16 rows run into first.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  const float2 f = unpack2(v);
+  return f.x + f.y;
+}
+
+// A 16-byte vector as P pairs
 template <typename T> struct Vec;
 template <> struct Vec<__nv_bfloat16> {
-  static constexpr int V = 8;
-  __device__ static void get(const uint4& q, float (&v)[8]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  static constexpr int V = 8, P = 4;
+  __device__ static f32x2 pair(const uint4& q, int i) {
+    const uint32_t w = i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w;
+    return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  __device__ static uint4 put(const f32x2 (&v)[4]) {
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      const float2 f = unpack2(v[i]);
+      w[i] = pack_bf16x2(f.x, f.y);
     }
-  }
-  __device__ static uint4 put(const float (&v)[8]) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <> struct Vec<float> {
-  static constexpr int V = 4;
-  __device__ static void get(const uint4& q, float (&v)[4]) {
-    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
-    v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+  static constexpr int V = 4, P = 2;
+  __device__ static f32x2 pair(const uint4& q, int i) {
+    return i == 0 ? pack2(__uint_as_float(q.x), __uint_as_float(q.y))
+                  : pack2(__uint_as_float(q.z), __uint_as_float(q.w));
   }
-  __device__ static uint4 put(const float (&v)[4]) {
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  __device__ static uint4 put(const f32x2 (&v)[2]) {
+    const float2 a = unpack2(v[0]), b = unpack2(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   }
 };
 
-__device__ __forceinline__ void copy16_async(uint4* dst, const uint4* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src) : "memory");
+__device__ __forceinline__ void copy16_async(uint32_t dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() {
@@ -135,249 +170,277 @@ template <int N> __device__ __forceinline__ void copy_wait() {
 }
 
 constexpr int kMaxTeam = 512;
+// The backward kernels hide their reductions with warps, so up to 16 elements
+// a thread two blocks of 384 threads share an SM (at most 80 registers); fp32
+// rows and rows of more than 6144 bf16 values run up to 512 threads with 128.
+__host__ __device__ constexpr int max_threads(int vpt) { return vpt == 4 ? kMaxTeam : 384; }
+__host__ __device__ constexpr int min_blocks(int vpt) { return vpt == 4 ? 1 : 2; }
+constexpr int kMaxWarps = kMaxTeam / 32;
 constexpr int kMaxRing = 224 * 1024;
-// row groups in shared memory, the current one included
-__host__ __device__ constexpr int stages_of(int vpt) { return vpt == 4 ? 2 : 3; }
+constexpr int kStages = 3;          // row groups in shared memory, the current one included
 
 // Sums of N values over the `tpr` threads of a team (whole warps), in every
-// thread: butterflies, then the warps' sums in order.  Two buffers in turn,
-// so one barrier a call is enough.
+// thread: a butterfly in each warp, then one over the warps' sums.  Two
+// buffers in turn, so one barrier a call is enough.
 template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], int tpr, float (*s_red)[kMaxTeam / 32][4], int& buf) {
+__device__ __forceinline__ void team_sum(float (&v)[N], int tpr, float4 (*s_red)[kMaxWarps], int& buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if (tpr == 32) return;            // uniform over the block
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s_red[buf][warp][i] = v[i];
-  __syncthreads();
-  const int first = static_cast<int>(threadIdx.x) / tpr * (tpr >> 5);
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.0f;
-  for (int w = 0; w < tpr >> 5; ++w) {
-    const float4 q = *reinterpret_cast<const float4*>(s_red[buf][first + w]);
-    const float a[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += a[i];
+  const int lane = threadIdx.x & 31, wpr = tpr >> 5;
+  if (lane == 0) {
+    float4 q = make_float4(v[0], 0.0f, 0.0f, 0.0f);
+    if (N > 1) q.y = v[N > 1 ? 1 : 0];
+    if (N > 2) q.z = v[N > 2 ? 2 : 0];
+    s_red[buf][threadIdx.x >> 5] = q;
   }
+  __syncthreads();
+  const int w = lane & (kMaxWarps - 1);
+  const float4 q = w < wpr ? s_red[buf][static_cast<int>(threadIdx.x) / tpr * wpr + w]
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  v[0] = q.x;
+  if (N > 1) v[N > 1 ? 1 : 0] = q.y;
+  if (N > 2) v[N > 2 ? 2 : 0] = q.z;
+#pragma unroll
+  for (int o = kMaxWarps / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   buf ^= 1;
 }
 
-// One thread's share of the row ring: ARR arrays of VPT vectors a row group.
-template <int VPT, int ARR> struct Ring {
-  uint4* base;
-  int threads;
-  __device__ __forceinline__ uint4* at(int stage, int arr, int j) const {
-    return base + ((stage * ARR + arr) * VPT + j) * threads + threadIdx.x;
+// What the row kernels share: this thread's place, and its own slots of the
+// ring ([stage][ARR * VPT][thread] vectors: a warp's copies and reads are runs
+// of 512 bytes).
+template <typename T, int VPT, int ARR> struct Team {
+  static constexpr int SLOTS = ARR * VPT;
+  int nv, tpr, team, me, rpb;
+  int64_t rows, step;
+  uint4* mine;                 // stage 0
+  uint32_t mine_smem;
+  int stage_vecs;              // vectors of a stage
+  __device__ __forceinline__ Team(int H, int tpr_, int64_t rows_, uint8_t* s_dyn)
+      : nv(H / Vec<T>::V), tpr(tpr_), rows(rows_) {
+    team = static_cast<int>(threadIdx.x) / tpr;
+    me = static_cast<int>(threadIdx.x) - team * tpr;
+    rpb = static_cast<int>(blockDim.x) / tpr;
+    step = static_cast<int64_t>(gridDim.x) * rpb;
+    mine = reinterpret_cast<uint4*>(s_dyn) + threadIdx.x;
+    mine_smem = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+    stage_vecs = static_cast<int>(blockDim.x) * SLOTS;
+    // vectors past the row's end stay zero: they add nothing to any sum
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) mine[s * stage_vecs + i * static_cast<int>(blockDim.x)] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ bool has(int j) const { return me + j * tpr < nv; }
+  __device__ __forceinline__ void fetch(const uint4* const (&src)[3], int64_t t, int stage) const {
+    if (t < rows) {
+      const int64_t at = t * nv + me;
+      const uint32_t dst = mine_smem + static_cast<uint32_t>(stage * stage_vecs) * 16;
+#pragma unroll
+      for (int a = 0; a < ARR; ++a)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+          if (has(j)) copy16_async(dst + (a * VPT + j) * blockDim.x * 16, src[a] + at + j * tpr);
+    }
+    copy_commit();
   }
 };
 
 template <typename T, int VPT>
-__global__ void __launch_bounds__(kMaxTeam)
+__global__ void __launch_bounds__(kMaxTeam, 2)
     layer_norm_rows_kernel(const T* x_, const T* __restrict__ w_, const T* __restrict__ b_, T* out_,
                            int64_t rows, int H, float eps, int tpr) {
-  constexpr int V = Vec<T>::V, kStages = stages_of(VPT);
+  constexpr int P = Vec<T>::P;
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  __shared__ __align__(16) float s_red[2][kMaxTeam / 32][4];
+  __shared__ float4 s_red[2][kMaxWarps];
   pdl_wait();
   pdl_trigger();
-  const Ring<VPT, 1> ring{reinterpret_cast<uint4*>(s_dyn), static_cast<int>(blockDim.x)};
-  const uint4* x = reinterpret_cast<const uint4*>(x_);
+  const Team<T, VPT, 1> tm(H, tpr, rows, s_dyn);
+  const uint4* const src[3] = {reinterpret_cast<const uint4*>(x_), nullptr, nullptr};
   const uint4* w = reinterpret_cast<const uint4*>(w_);
   const uint4* bias = reinterpret_cast<const uint4*>(b_);
   uint4* out = reinterpret_cast<uint4*>(out_);
-  const int nv = H / V, team = static_cast<int>(threadIdx.x) / tpr, me = static_cast<int>(threadIdx.x) - team * tpr;
-  const int rpb = static_cast<int>(blockDim.x) / tpr;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
   const float inv_h = 1.0f / static_cast<float>(H);
-  auto fetch = [&](int64_t t, int stage) {
+  int64_t base = static_cast<int64_t>(blockIdx.x) * tm.rpb;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) tm.fetch(src, base + s * tm.step + tm.team, s);
+  int stage = 0, buf = 0;
+  for (; base < rows; base += tm.step) {
+    const int64_t t = base + tm.team;
+    tm.fetch(src, t + (kStages - 1) * tm.step, stage == 0 ? kStages - 1 : stage - 1);
+    copy_wait<kStages - 1>();
+    const uint4* ring = tm.mine + stage * tm.stage_vecs;
+    f32x2 xc[VPT][P], acc = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const uint4 q = ring[j * static_cast<int>(blockDim.x)];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        xc[j][i] = Vec<T>::pair(q, i);
+        acc = add2(acc, xc[j][i]);
+      }
+    }
+    float s1[1] = {sum2(acc)};
+    team_sum<1>(s1, tpr, s_red, buf);
+    const float mean = s1[0] * inv_h;
+    const f32x2 neg_mean = pack2(-mean, -mean);
+    acc = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+      if (tm.has(j))
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          xc[j][i] = add2(xc[j][i], neg_mean);
+          acc = fma2(xc[j][i], xc[j][i], acc);
+        }
+    float s2[1] = {sum2(acc)};
+    team_sum<1>(s2, tpr, s_red, buf);
+    const float r = rsqrtf(s2[0] * inv_h + eps);
+    const f32x2 r2 = pack2(r, r);
     if (t < rows)
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
-        if (me + j * tpr < nv) copy16_async(ring.at(stage, 0, j), x + t * nv + me + j * tpr);
-    copy_commit();
-  };
-  int64_t base = static_cast<int64_t>(blockIdx.x) * rpb;
+        if (tm.has(j)) {
+          const int c = tm.me + j * tpr;
+          const uint4 wq = w[c], bq = bias != nullptr ? bias[c] : make_uint4(0, 0, 0, 0);
+          f32x2 y[P];
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(base + s * step + team, s);
-  int stage = 0, buf = 0;
-  for (; base < rows; base += step) {
-    const int64_t t = base + team;
-    fetch(t + (kStages - 1) * step, (stage + kStages - 1) % kStages);
-    copy_wait<kStages - 1>();
-    float xv[VPT][V];
-    float s1[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const bool mine = t < rows && me + j * tpr < nv;
-      const uint4 q = mine ? *ring.at(stage, 0, j) : make_uint4(0, 0, 0, 0);
-      Vec<T>::get(q, xv[j]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s1[0] += xv[j][i];
-    }
-    team_sum<1>(s1, tpr, s_red, buf);
-    const float mean = s1[0] * inv_h;
-    float s2[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (me + j * tpr < nv)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          xv[j][i] -= mean;
-          s2[0] = fmaf(xv[j][i], xv[j][i], s2[0]);
+          for (int i = 0; i < P; ++i)
+            y[i] = fma2(mul2(xc[j][i], r2), Vec<T>::pair(wq, i), Vec<T>::pair(bq, i));
+          out[t * tm.nv + c] = Vec<T>::put(y);
         }
-    team_sum<1>(s2, tpr, s_red, buf);
-    const float r = 1.0f / sqrtf(s2[0] * inv_h + eps);
-    if (t < rows)
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = me + j * tpr;
-        if (c >= nv) continue;
-        float wv[V], bv[V];
-        Vec<T>::get(w[c], wv);
-        Vec<T>::get(bias != nullptr ? bias[c] : make_uint4(0, 0, 0, 0), bv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) xv[j][i] = fmaf(xv[j][i] * r, wv[i], bv[i]);
-        out[t * nv + c] = Vec<T>::put(xv[j]);
-      }
-    stage = (stage + 1) % kStages;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   copy_wait<0>();
 }
 
 template <typename T, int VPT, bool LAYER, bool RES>
-__global__ void __launch_bounds__(kMaxTeam)
+__global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
     norm_backward_rows_kernel(const T* x_, const T* __restrict__ w_, const T* dout_, const T* dres_, T* dx_,
                               float* __restrict__ part_w, float* __restrict__ part_b, int64_t rows, int H,
                               float eps, int tpr) {
-  constexpr int V = Vec<T>::V, ARR = RES ? 3 : 2, kStages = stages_of(VPT);
+  constexpr int P = Vec<T>::P, ARR = RES ? 3 : 2;
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  __shared__ __align__(16) float s_red[2][kMaxTeam / 32][4];
+  __shared__ float4 s_red[2][kMaxWarps];
   pdl_wait();
   pdl_trigger();
-  const Ring<VPT, ARR> ring{reinterpret_cast<uint4*>(s_dyn), static_cast<int>(blockDim.x)};
-  const uint4* src[3] = {reinterpret_cast<const uint4*>(x_), reinterpret_cast<const uint4*>(dout_),
-                         reinterpret_cast<const uint4*>(dres_)};
+  const Team<T, VPT, ARR> tm(H, tpr, rows, s_dyn);
+  const uint4* const src[3] = {reinterpret_cast<const uint4*>(x_), reinterpret_cast<const uint4*>(dout_),
+                               reinterpret_cast<const uint4*>(dres_)};
   uint4* dx = reinterpret_cast<uint4*>(dx_);
-  const int nv = H / V, team = static_cast<int>(threadIdx.x) / tpr, me = static_cast<int>(threadIdx.x) - team * tpr;
-  const int rpb = static_cast<int>(blockDim.x) / tpr;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rpb;
   const float inv_h = 1.0f / static_cast<float>(H);
-  auto fetch = [&](int64_t t, int stage) {
-    if (t < rows)
+  int64_t base = static_cast<int64_t>(blockIdx.x) * tm.rpb;
 #pragma unroll
-      for (int a = 0; a < ARR; ++a)
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-          if (me + j * tpr < nv) copy16_async(ring.at(stage, a, j), src[a] + t * nv + me + j * tpr);
-    copy_commit();
-  };
-  int64_t base = static_cast<int64_t>(blockIdx.x) * rpb;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) fetch(base + s * step + team, s);
+  for (int s = 0; s < kStages - 1; ++s) tm.fetch(src, base + s * tm.step + tm.team, s);
   uint4 wq[VPT];
-  float aw[VPT][V], ab[VPT][V];
+  f32x2 aw[VPT][P], ab[VPT][P];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    wq[j] = me + j * tpr < nv ? reinterpret_cast<const uint4*>(w_)[me + j * tpr] : make_uint4(0, 0, 0, 0);
+    wq[j] = tm.has(j) ? reinterpret_cast<const uint4*>(w_)[tm.me + j * tpr] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < V; ++i) aw[j][i] = ab[j][i] = 0.0f;
+    for (int i = 0; i < P; ++i) aw[j][i] = ab[j][i] = 0;
   }
   int stage = 0, buf = 0;
-  for (; base < rows; base += step) {
-    const int64_t t = base + team;
-    fetch(t + (kStages - 1) * step, (stage + kStages - 1) % kStages);
+  for (; base < rows; base += tm.step) {
+    const int64_t t = base + tm.team;
+    tm.fetch(src, t + (kStages - 1) * tm.step, stage == 0 ? kStages - 1 : stage - 1);
     copy_wait<kStages - 1>();
-    // vectors past the row, and rows past the last, read as zeros: they add
-    // nothing to any sum (the mean is taken off live elements alone)
-    uint4 xq[VPT], gq[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const bool mine = t < rows && me + j * tpr < nv;
-      xq[j] = mine ? *ring.at(stage, 0, j) : make_uint4(0, 0, 0, 0);
-      gq[j] = mine ? *ring.at(stage, 1, j) : make_uint4(0, 0, 0, 0);
-    }
+    const uint4* ring = tm.mine + stage * tm.stage_vecs;
+    // each pass reads the row from shared memory again: registers for 16 more
+    // fp32 values would cost the second block of the SM
+    auto read = [&](int a, int j) { return ring[(a * VPT + j) * static_cast<int>(blockDim.x)]; };
     float mean = 0.0f;
     if (LAYER) {
-      float s1[1] = {0.0f};
+      f32x2 acc = 0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        float xv[V];
-        Vec<T>::get(xq[j], xv);
+        const uint4 xq = read(0, j);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s1[0] += xv[i];
+        for (int i = 0; i < P; ++i) acc = add2(acc, Vec<T>::pair(xq, i));
       }
+      float s1[1] = {sum2(acc)};
       team_sum<1>(s1, tpr, s_red, buf);
       mean = s1[0] * inv_h;
     }
-    float s[LAYER ? 3 : 2] = {};          // x'^2, gy x', and gy (x' = x - mean)
+    const f32x2 neg_mean = pack2(-mean, -mean);
+    f32x2 sxx = 0, sgx = 0, sg = 0;       // x'^2, gy x', gy   (x' = x - mean)
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (me + j * tpr >= nv) continue;
-      float xv[V], gv[V], wv[V];
-      Vec<T>::get(xq[j], xv);
-      Vec<T>::get(gq[j], gv);
-      Vec<T>::get(wq[j], wv);
+    for (int j = 0; j < VPT; ++j)
+      if (!LAYER || tm.has(j)) {
+        const uint4 xq = read(0, j), gq = read(1, j);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xc = xv[i] - mean, gy = gv[i] * wv[i];
-        s[0] = fmaf(xc, xc, s[0]);
-        s[1] = fmaf(gy, xc, s[1]);
-        if (LAYER) s[LAYER ? 2 : 0] += gy;
+        for (int i = 0; i < P; ++i) {
+          f32x2 xc = Vec<T>::pair(xq, i);
+          if (LAYER) xc = add2(xc, neg_mean);
+          const f32x2 gy = mul2(Vec<T>::pair(gq, i), Vec<T>::pair(wq[j], i));
+          sxx = fma2(xc, xc, sxx);
+          sgx = fma2(gy, xc, sgx);
+          if (LAYER) sg = add2(sg, gy);
+        }
       }
-    }
+    float s[LAYER ? 3 : 2];
+    s[0] = sum2(sxx);
+    s[1] = sum2(sgx);
+    if (LAYER) s[LAYER ? 2 : 0] = sum2(sg);
     team_sum<LAYER ? 3 : 2>(s, tpr, s_red, buf);
-    const float r = 1.0f / sqrtf(s[0] * inv_h + eps);
-    const float m1 = LAYER ? s[LAYER ? 2 : 0] * inv_h : 0.0f, m2 = s[1] * r * inv_h;
+    // dx = r gy - r mean(gy) - k x',  k = r^3 mean(gy x')
+    const float r = rsqrtf(s[0] * inv_h + eps);
+    const float k = -r * (r * (r * (s[1] * inv_h)));
+    const float m1 = LAYER ? -r * (s[LAYER ? 2 : 0] * inv_h) : 0.0f;
+    const f32x2 r2 = pack2(r, r), k2 = pack2(k, k), m12 = pack2(m1, m1);
     if (t < rows)
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int c = me + j * tpr;
-        if (c >= nv) continue;
-        float xv[V], gv[V], wv[V], dv[V];
-        Vec<T>::get(xq[j], xv);
-        Vec<T>::get(gq[j], gv);
-        Vec<T>::get(wq[j], wv);
-        if (RES) Vec<T>::get(*ring.at(stage, ARR - 1, j), dv);
+      for (int j = 0; j < VPT; ++j)
+        if (tm.has(j)) {
+          const uint4 xq = read(0, j), gq = read(1, j);
+          uint4 dq = make_uint4(0, 0, 0, 0);
+          if (RES) dq = read(ARR - 1, j);
+          f32x2 d[P];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (xv[i] - mean) * r;
-          aw[j][i] = fmaf(gv[i], xh, aw[j][i]);
-          if (LAYER) ab[j][i] += gv[i];
-          const float d = r * (gv[i] * wv[i] - m1 - xh * m2);
-          dv[i] = RES ? dv[i] + d : d;
+          for (int i = 0; i < P; ++i) {
+            f32x2 xc = Vec<T>::pair(xq, i);
+            if (LAYER) xc = add2(xc, neg_mean);
+            const f32x2 g = Vec<T>::pair(gq, i);
+            aw[j][i] = fma2(g, mul2(xc, r2), aw[j][i]);
+            if (LAYER) ab[j][i] = add2(ab[j][i], g);
+            f32x2 v = LAYER ? fma2(xc, k2, m12) : mul2(xc, k2);
+            v = fma2(mul2(g, Vec<T>::pair(wq[j], i)), r2, v);
+            d[i] = RES ? add2(v, Vec<T>::pair(dq, i)) : v;
+          }
+          dx[t * tm.nv + tm.me + j * tpr] = Vec<T>::put(d);
         }
-        dx[t * nv + c] = Vec<T>::put(dv);
-      }
-    stage = (stage + 1) % kStages;
+    stage = stage == kStages - 1 ? 0 : stage + 1;
   }
   copy_wait<0>();
   // the teams' sums, in order, through shared memory (the ring is done)
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * H;
   float* s_sum = reinterpret_cast<float*>(s_dyn);
 #pragma unroll
   for (int pass = 0; pass < (LAYER ? 2 : 1); ++pass) {
     float* part = pass == 0 ? part_w : part_b;
     if (part == nullptr) continue;        // uniform
-    for (int turn = 0; turn < rpb; ++turn) {
+    part += static_cast<int64_t>(blockIdx.x) * H;
+    for (int turn = 0; turn < tm.rpb; ++turn) {
       __syncthreads();
-      if (team == turn)
+      if (tm.team == turn)
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-          const int c = (me + j * tpr) * V;
-          if (c >= H) continue;
+        for (int j = 0; j < VPT; ++j)
+          if (tm.has(j))
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float v = pass == 0 ? aw[j][i] : ab[j][i];
-            if (turn > 0) v = s_sum[c + i] + v;
-            if (turn + 1 < rpb) s_sum[c + i] = v;
-            else part[at + c + i] = v;
-          }
-        }
+            for (int i = 0; i < P; ++i) {
+              const int c = (tm.me + j * tpr) * Vec<T>::V + 2 * i;
+              float2 v = unpack2(pass == 0 ? aw[j][i] : ab[j][i]);
+              if (turn > 0) {
+                v.x = s_sum[c] + v.x;
+                v.y = s_sum[c + 1] + v.y;
+              }
+              *reinterpret_cast<float2*>((turn + 1 < tm.rpb ? s_sum : part) + c) = v;
+            }
     }
+    __syncthreads();
   }
 }
 
@@ -418,13 +481,13 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // out[c] = sum over blocks of part[block][c]: 32 columns a block of threads,
-// warp w adds the partial rows w, w + 8, ... in order, then the warps' sums
-// are added in order.
-__global__ void __launch_bounds__(kThreads)
+// warp w adds the partial rows w, w + 32, ... in order, then the warps' sums
+// are added in a fixed tree.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps)
     norm_partials_kernel(const float* __restrict__ part_w, const float* __restrict__ part_b, int blocks,
                          int H, float* __restrict__ dweight, float* __restrict__ dbias) {
-  constexpr int W = kThreads / 32;
-  __shared__ float s_sum[W][32];
+  __shared__ float s_sum[kSumWarps][33];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -432,40 +495,42 @@ __global__ void __launch_bounds__(kThreads)
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float s = 0.0f;
   if (c < H) {
-    int b = warp;
-    for (; b + 7 * W < blocks; b += 8 * W) {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = part[static_cast<int64_t>(b + i * W) * H + c];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
-    }
-    for (; b < blocks; b += W) s += part[static_cast<int64_t>(b) * H + c];
+#pragma unroll 4
+    for (int b = warp; b < blocks; b += kSumWarps) s += part[static_cast<int64_t>(b) * H + c];
   }
   s_sum[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < H) {
-    float t = 0.0f;
+  // warp w: column w, over the warps' sums
+  float t = s_sum[lane][warp];
 #pragma unroll
-    for (int w = 0; w < W; ++w) t += s_sum[w][lane];
-    (blockIdx.y == 0 ? dweight : dbias)[c] = t;
-  }
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const int cw = blockIdx.x * 32 + warp;
+  if (lane == 0 && cw < H) (blockIdx.y == 0 ? dweight : dbias)[cw] = t;
 }
 
 // Threads of a team and the vectors each holds; 0 vectors: the row has no
 // whole 16-byte vectors or is too long for a team.
 struct TeamShape {
   int vpt, tpr, threads;
+  int rows_a_block() const { return threads / tpr; }
 };
 template <typename T> TeamShape team_shape(int H) {
-  constexpr int V = Vec<T>::V, want = 16 / V;        // 16 elements a thread
+  constexpr int V = Vec<T>::V;
   TeamShape s{0, 0, 0};
   if (H % V != 0 || H / V > 4 * kMaxTeam) return s;
   const int nv = H / V;
-  s.vpt = nv <= 32 ? 1 : nv <= want * kMaxTeam ? want : 4;
-  s.tpr = (static_cast<int>(ceil_div(nv, s.vpt)) + 31) / 32 * 32;
-  s.threads = s.tpr >= 256 ? s.tpr : 256 / s.tpr * s.tpr;
+  s.vpt = nv <= 32 ? 1 : V == 8 && nv <= 2 * 384 ? 2 : V == 4 && nv <= 64 ? 2 : 4;
+  s.tpr = static_cast<int>(ceil_div(ceil_div(nv, s.vpt), 32) * 32);
+  const int full = s.vpt == 4 ? 256 : 384;
+  s.threads = s.tpr >= full ? s.tpr : full / s.tpr * s.tpr;
   return s;
+}
+// shared memory of a block, and the blocks an SM holds
+size_t ring_bytes(const TeamShape& s, int arrays) {
+  return static_cast<size_t>(kStages) * arrays * s.vpt * s.threads * 16;
+}
+int resident_blocks(int threads_by_regs, const TeamShape& s, size_t smem) {
+  return std::max(1, std::min(static_cast<int>(kMaxRing / (smem + 2048)), threads_by_regs / s.threads));
 }
 
 // more than 48 KB of shared memory (some of it static) has to be asked for,
@@ -485,20 +550,20 @@ template <auto Kernel> cudaError_t allow_smem(size_t bytes) {
 template <typename T, int VPT>
 cudaError_t forward_rows(const TeamShape& s, int64_t rows, int H, float eps, const void* x, const void* w,
                          const void* b, void* out, int num_sms, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(stages_of(VPT)) * VPT * s.threads * 16;
+  const size_t smem = ring_bytes(s, 1);
   const cudaError_t e = allow_smem<layer_norm_rows_kernel<T, VPT>>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t groups = ceil_div(rows, s.threads / s.tpr);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(groups, static_cast<int64_t>(num_sms) * (1024 / s.threads)));
-  return launch_chained(layer_norm_rows_kernel<T, VPT>, grid, s.threads, smem, stream, static_cast<const T*>(x), static_cast<const T*>(w),
-                        static_cast<const T*>(b), static_cast<T*>(out), rows, H, eps, s.tpr);
+  const int64_t groups = ceil_div(rows, s.rows_a_block());
+  const unsigned grid = static_cast<unsigned>(
+      std::min<int64_t>(groups, static_cast<int64_t>(num_sms) * resident_blocks(2 * kMaxTeam, s, smem)));
+  return launch_chained(layer_norm_rows_kernel<T, VPT>, grid, s.threads, smem, stream, static_cast<const T*>(x),
+                        static_cast<const T*>(w), static_cast<const T*>(b), static_cast<T*>(out), rows, H, eps,
+                        s.tpr);
 }
 
 template <typename T, int VPT, bool LAYER, bool RES>
-cudaError_t backward_rows(const TeamShape& s, const NormBackwardArgs& a, float* part_b, int blocks,
+cudaError_t backward_rows(const TeamShape& s, const NormBackwardArgs& a, float* part_b, int blocks, size_t smem,
                           cudaStream_t stream) {
-  size_t smem = static_cast<size_t>(stages_of(VPT)) * (RES ? 3 : 2) * VPT * s.threads * 16;
-  smem = std::max(smem, static_cast<size_t>(a.H) * sizeof(float));
   const cudaError_t e = allow_smem<norm_backward_rows_kernel<T, VPT, LAYER, RES>>(smem);
   if (e != cudaSuccess) return e;
   return launch_chained(norm_backward_rows_kernel<T, VPT, LAYER, RES>, static_cast<unsigned>(blocks), s.threads,
@@ -508,13 +573,13 @@ cudaError_t backward_rows(const TeamShape& s, const NormBackwardArgs& a, float* 
 }
 
 template <typename T, int VPT>
-cudaError_t backward_rows_of(const TeamShape& s, const NormBackwardArgs& a, float* part_b, int blocks,
+cudaError_t backward_rows_of(const TeamShape& s, const NormBackwardArgs& a, float* part_b, int blocks, size_t smem,
                              cudaStream_t stream) {
   if (a.layer)
-    return a.dres != nullptr ? backward_rows<T, VPT, true, true>(s, a, part_b, blocks, stream)
-                             : backward_rows<T, VPT, true, false>(s, a, part_b, blocks, stream);
-  return a.dres != nullptr ? backward_rows<T, VPT, false, true>(s, a, part_b, blocks, stream)
-                           : backward_rows<T, VPT, false, false>(s, a, part_b, blocks, stream);
+    return a.dres != nullptr ? backward_rows<T, VPT, true, true>(s, a, part_b, blocks, smem, stream)
+                             : backward_rows<T, VPT, true, false>(s, a, part_b, blocks, smem, stream);
+  return a.dres != nullptr ? backward_rows<T, VPT, false, true>(s, a, part_b, blocks, smem, stream)
+                           : backward_rows<T, VPT, false, false>(s, a, part_b, blocks, smem, stream);
 }
 
 template <typename T>
@@ -544,13 +609,16 @@ cudaError_t forward_of(int64_t rows, int H, float eps, const void* x, const void
 template <typename T>
 cudaError_t backward_of(const NormBackwardArgs& a, float* part_b, int num_sms, int* blocks, cudaStream_t stream) {
   const TeamShape s = team_shape<T>(a.H);
-  const int64_t groups = s.vpt == 0 ? a.T : ceil_div(a.T, s.threads / s.tpr);
-  const int64_t resident = static_cast<int64_t>(num_sms) * (s.vpt == 0 ? 4 : s.threads <= 384 ? 2 : 1);
+  const size_t smem = s.vpt == 0 ? 0 : std::max(ring_bytes(s, a.dres != nullptr ? 3 : 2),
+                                                static_cast<size_t>(a.H) * sizeof(float));
+  const bool team = s.vpt != 0 && smem <= kMaxRing;
+  const int64_t groups = team ? ceil_div(a.T, s.rows_a_block()) : a.T;
+  const int64_t resident = static_cast<int64_t>(num_sms) * (team ? resident_blocks(max_threads(s.vpt) * min_blocks(s.vpt), s, smem) : 4);
   *blocks = static_cast<int>(std::min<int64_t>(groups, std::min<int64_t>(resident, kNormMaxBlocks)));
   if (*blocks == 0) return cudaSuccess;
-  if (s.vpt == 1) return backward_rows_of<T, 1>(s, a, part_b, *blocks, stream);
-  if (s.vpt == 2) return backward_rows_of<T, 2>(s, a, part_b, *blocks, stream);
-  if (s.vpt == 4) return backward_rows_of<T, 4>(s, a, part_b, *blocks, stream);
+  if (team && s.vpt == 1) return backward_rows_of<T, 1>(s, a, part_b, *blocks, smem, stream);
+  if (team && s.vpt == 2) return backward_rows_of<T, 2>(s, a, part_b, *blocks, smem, stream);
+  if (team && s.vpt == 4) return backward_rows_of<T, 4>(s, a, part_b, *blocks, smem, stream);
   return backward_any<T>(a, *blocks, part_b, stream);
 }
 
@@ -570,7 +638,7 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int num_sms, cudaStr
                                             : backward_of<float>(a, part_b, num_sms, &blocks, stream);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(ceil_div(a.H, 32)), a.dbias != nullptr ? 2 : 1);
-  return launch_chained(norm_partials_kernel, grid, dim3(kThreads), 0, stream,
+  return launch_chained(norm_partials_kernel, grid, dim3(32 * kSumWarps), 0, stream,
                         static_cast<const float*>(a.partials), static_cast<const float*>(part_b), blocks,
                         a.H, a.dweight, a.dbias);
 }
