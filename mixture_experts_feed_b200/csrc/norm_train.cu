@@ -21,8 +21,9 @@
 // copies its own vectors of the rows to come into shared memory with cp.async,
 // two row groups ahead, and reads back only what it copied itself: the
 // loads stay in flight across the reductions with no barrier between them.
-// The reductions (RMSNorm one, layer norm two: the mean first) cost one block
-// barrier each, none when a team is one warp.  Other rows take the *_any
+// A row costs one reduction with one block barrier (none when a team is one
+// warp): layer norm's mean of the next row is summed with the current row's
+// other sums.  Other rows take the *_any
 // kernels, which stream them several times.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -173,47 +174,77 @@ constexpr int kMaxTeam = 512;
 // The backward kernels hide their reductions with warps, so up to 16 elements
 // a thread two blocks of 384 threads share an SM (at most 80 registers); fp32
 // rows and rows of more than 6144 bf16 values run up to 512 threads with 128.
-__host__ __device__ constexpr int max_threads(int vpt) { return vpt == 4 ? kMaxTeam : 384; }
-__host__ __device__ constexpr int min_blocks(int vpt) { return vpt == 4 ? 1 : 2; }
-constexpr int kMaxWarps = kMaxTeam / 32;
+__host__ __device__ constexpr int max_threads(int vpt) { return vpt == 4 ? kMaxTeam : vpt == 1 ? 768 : 384; }
+__host__ __device__ constexpr int min_blocks(int vpt) { return vpt == 2 ? 2 : 1; }
+constexpr int kMaxWarps = 32;
 constexpr int kMaxRing = 224 * 1024;
-constexpr int kStages = 3;          // row groups in shared memory, the current one included
+// row groups in shared memory, the current one included (layer norm also reads
+// the next one; with three arrays a fourth would not leave room for two blocks)
+__host__ __device__ constexpr int stages_of(bool layer, int arrays) { return layer && arrays < 3 ? 4 : 3; }
 
-// Sums of N values over the `tpr` threads of a team (whole warps), in every
-// thread: a butterfly in each warp, then one over the warps' sums.  Two
-// buffers in turn, so one barrier a call is enough.
+// Sums of N values (1, 2 or 4) over the `tpr` threads of a team (whole warps;
+// at most 16 for two values), in every thread: in each warp, then, past one
+// barrier, over the warps' sums.  Two buffers in turn, so one barrier a call is
+// enough.  One or two values go by butterflies; four are scattered over the
+// lanes as they are summed (the first exchange leaves each lane 2 of them, the
+// second 1, three more steps finish: 6 shuffles instead of 20), summed over
+// the warps side by side, and broadcast.
 template <int N>
-__device__ __forceinline__ void team_sum(float (&v)[N], int tpr, float4 (*s_red)[kMaxWarps], int& buf) {
+__device__ __forceinline__ void team_sum(float (&v)[N], int tpr, float (*s_red)[4 * kMaxWarps], int& buf) {
+  static_assert(N == 1 || N == 2 || N == 4, "");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wpr = tpr >> 5;
+  if (N <= 2) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+    for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if (tpr == 32) return;            // uniform over the block
-  const int lane = threadIdx.x & 31, wpr = tpr >> 5;
-  if (lane == 0) {
-    float4 q = make_float4(v[0], 0.0f, 0.0f, 0.0f);
-    if (N > 1) q.y = v[N > 1 ? 1 : 0];
-    if (N > 2) q.z = v[N > 2 ? 2 : 0];
-    s_red[buf][threadIdx.x >> 5] = q;
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (tpr == 32) return;          // uniform over the block
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s_red[buf][warp * N + i] = v[i];
+    __syncthreads();
+    constexpr int W = kMaxWarps / N;
+    const int w = lane & (W - 1);
+    const float* part = s_red[buf] + (warp - warp % wpr + w) * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = w < wpr ? part[i] : 0.0f;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    buf ^= 1;
+    return;
   }
-  __syncthreads();
-  const int w = lane & (kMaxWarps - 1);
-  const float4 q = w < wpr ? s_red[buf][static_cast<int>(threadIdx.x) / tpr * wpr + w]
-                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  v[0] = q.x;
-  if (N > 1) v[N > 1 ? 1 : 0] = q.y;
-  if (N > 2) v[N > 2 ? 2 : 0] = q.z;
+  const bool b0 = lane & 1, b1 = lane & 2;
+  const int id = (b0 ? 2 : 0) + (b1 ? 1 : 0);   // the value this lane ends up with
+  const float k0 = b0 ? v[N > 2 ? 2 : 0] : v[0], k1 = b0 ? v[N > 3 ? 3 : 0] : v[N > 1 ? 1 : 0];
+  const float g0 = b0 ? v[0] : v[N > 2 ? 2 : 0], g1 = b0 ? v[N > 1 ? 1 : 0] : v[N > 3 ? 3 : 0];
+  const float c0 = k0 + __shfl_xor_sync(0xffffffffu, g0, 1), c1 = k1 + __shfl_xor_sync(0xffffffffu, g1, 1);
+  float a = (b1 ? c1 : c0) + __shfl_xor_sync(0xffffffffu, b1 ? c0 : c1, 2);
 #pragma unroll
-  for (int o = kMaxWarps / 2; o > 0; o >>= 1)
+  for (int o = 4; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (tpr > 32) {                   // uniform over the block
+    if (lane < 4) s_red[buf][warp * 4 + id] = a;
+    __syncthreads();
+    const float* part = s_red[buf] + (warp - warp % wpr) * 4 + id;
+    a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  buf ^= 1;
+    for (int w = 0; w < kMaxWarps; w += 8)
+      if (w + (lane >> 2) < wpr) a += part[(w + (lane >> 2)) * 4];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    buf ^= 1;
+  }
+  v[0] = __shfl_sync(0xffffffffu, a, 0);
+  v[N > 1 ? 1 : 0] = __shfl_sync(0xffffffffu, a, 2);
+  v[N > 2 ? 2 : 0] = __shfl_sync(0xffffffffu, a, 1);
+  v[N > 3 ? 3 : 0] = __shfl_sync(0xffffffffu, a, 3);
 }
 
 // What the row kernels share: this thread's place, and its own slots of the
 // ring ([stage][ARR * VPT][thread] vectors: a warp's copies and reads are runs
 // of 512 bytes).
-template <typename T, int VPT, int ARR> struct Team {
+template <typename T, int VPT, int ARR, int STAGES> struct Team {
   static constexpr int SLOTS = ARR * VPT;
   int nv, tpr, team, me, rpb;
   int64_t rows, step;
@@ -231,7 +262,7 @@ template <typename T, int VPT, int ARR> struct Team {
     stage_vecs = static_cast<int>(blockDim.x) * SLOTS;
     // vectors past the row's end stay zero: they add nothing to any sum
 #pragma unroll
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < STAGES; ++s)
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i) mine[s * stage_vecs + i * static_cast<int>(blockDim.x)] = make_uint4(0, 0, 0, 0);
   }
@@ -248,6 +279,18 @@ template <typename T, int VPT, int ARR> struct Team {
     }
     copy_commit();
   }
+  __device__ __forceinline__ const uint4* slot(int stage) const { return mine + stage * stage_vecs; }
+  // this thread's share of the sum of the row in a stage
+  __device__ __forceinline__ float row_sum(int stage) const {
+    f32x2 acc = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const uint4 q = slot(stage)[j * static_cast<int>(blockDim.x)];
+#pragma unroll
+      for (int i = 0; i < Vec<T>::P; ++i) acc = add2(acc, Vec<T>::pair(q, i));
+    }
+    return sum2(acc);
+  }
 };
 
 template <typename T, int VPT>
@@ -256,10 +299,11 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
                            int64_t rows, int H, float eps, int tpr) {
   constexpr int P = Vec<T>::P;
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  __shared__ float4 s_red[2][kMaxWarps];
+  __shared__ float s_red[2][4 * kMaxWarps];
   pdl_wait();
   pdl_trigger();
-  const Team<T, VPT, 1> tm(H, tpr, rows, s_dyn);
+  constexpr int STAGES = stages_of(true, 1);
+  const Team<T, VPT, 1, STAGES> tm(H, tpr, rows, s_dyn);
   const uint4* const src[3] = {reinterpret_cast<const uint4*>(x_), nullptr, nullptr};
   const uint4* w = reinterpret_cast<const uint4*>(w_);
   const uint4* bias = reinterpret_cast<const uint4*>(b_);
@@ -267,38 +311,34 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   const float inv_h = 1.0f / static_cast<float>(H);
   int64_t base = static_cast<int64_t>(blockIdx.x) * tm.rpb;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) tm.fetch(src, base + s * tm.step + tm.team, s);
+  for (int s = 0; s < STAGES - 1; ++s) tm.fetch(src, base + s * tm.step + tm.team, s);
+  // the mean of the first row; every later one comes with the reduction of
+  // the row before it
   int stage = 0, buf = 0;
+  copy_wait<STAGES - 2>();
+  float s1[1] = {tm.row_sum(0)};
+  team_sum<1>(s1, tpr, s_red, buf);
+  float mean = s1[0] * inv_h;
   for (; base < rows; base += tm.step) {
     const int64_t t = base + tm.team;
-    tm.fetch(src, t + (kStages - 1) * tm.step, stage == 0 ? kStages - 1 : stage - 1);
-    copy_wait<kStages - 1>();
-    const uint4* ring = tm.mine + stage * tm.stage_vecs;
+    const int after = stage == STAGES - 1 ? 0 : stage + 1;
+    tm.fetch(src, t + (STAGES - 1) * tm.step, stage == 0 ? STAGES - 1 : stage - 1);
+    copy_wait<STAGES - 2>();
+    const f32x2 neg_mean = pack2(-mean, -mean);
     f32x2 xc[VPT][P], acc = 0;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const uint4 q = ring[j * static_cast<int>(blockDim.x)];
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        xc[j][i] = Vec<T>::pair(q, i);
-        acc = add2(acc, xc[j][i]);
-      }
-    }
-    float s1[1] = {sum2(acc)};
-    team_sum<1>(s1, tpr, s_red, buf);
-    const float mean = s1[0] * inv_h;
-    const f32x2 neg_mean = pack2(-mean, -mean);
-    acc = 0;
-#pragma unroll
     for (int j = 0; j < VPT; ++j)
-      if (tm.has(j))
+      if (tm.has(j)) {
+        const uint4 q = tm.slot(stage)[j * static_cast<int>(blockDim.x)];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          xc[j][i] = add2(xc[j][i], neg_mean);
+          xc[j][i] = add2(Vec<T>::pair(q, i), neg_mean);
           acc = fma2(xc[j][i], xc[j][i], acc);
         }
-    float s2[1] = {sum2(acc)};
-    team_sum<1>(s2, tpr, s_red, buf);
+      }
+    float s2[2] = {sum2(acc), tm.row_sum(after)};
+    team_sum<2>(s2, tpr, s_red, buf);
+    mean = s2[1] * inv_h;
     const float r = rsqrtf(s2[0] * inv_h + eps);
     const f32x2 r2 = pack2(r, r);
     if (t < rows)
@@ -313,7 +353,7 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
             y[i] = fma2(mul2(xc[j][i], r2), Vec<T>::pair(wq, i), Vec<T>::pair(bq, i));
           out[t * tm.nv + c] = Vec<T>::put(y);
         }
-    stage = stage == kStages - 1 ? 0 : stage + 1;
+    stage = after;
   }
   copy_wait<0>();
 }
@@ -323,19 +363,19 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
     norm_backward_rows_kernel(const T* x_, const T* __restrict__ w_, const T* dout_, const T* dres_, T* dx_,
                               float* __restrict__ part_w, float* __restrict__ part_b, int64_t rows, int H,
                               float eps, int tpr) {
-  constexpr int P = Vec<T>::P, ARR = RES ? 3 : 2;
+  constexpr int P = Vec<T>::P, ARR = RES ? 3 : 2, STAGES = stages_of(LAYER, ARR);
   extern __shared__ __align__(16) uint8_t s_dyn[];
-  __shared__ float4 s_red[2][kMaxWarps];
+  __shared__ float s_red[2][4 * kMaxWarps];
   pdl_wait();
   pdl_trigger();
-  const Team<T, VPT, ARR> tm(H, tpr, rows, s_dyn);
+  const Team<T, VPT, ARR, STAGES> tm(H, tpr, rows, s_dyn);
   const uint4* const src[3] = {reinterpret_cast<const uint4*>(x_), reinterpret_cast<const uint4*>(dout_),
                                reinterpret_cast<const uint4*>(dres_)};
   uint4* dx = reinterpret_cast<uint4*>(dx_);
   const float inv_h = 1.0f / static_cast<float>(H);
   int64_t base = static_cast<int64_t>(blockIdx.x) * tm.rpb;
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) tm.fetch(src, base + s * tm.step + tm.team, s);
+  for (int s = 0; s < STAGES - 1; ++s) tm.fetch(src, base + s * tm.step + tm.team, s);
   uint4 wq[VPT];
   f32x2 aw[VPT][P], ab[VPT][P];
 #pragma unroll
@@ -345,27 +385,23 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
     for (int i = 0; i < P; ++i) aw[j][i] = ab[j][i] = 0;
   }
   int stage = 0, buf = 0;
+  float mean = 0.0f;                      // of the current row
+  if (LAYER) {
+    // of the first row; every later one comes with the sums of the row before
+    copy_wait<STAGES - 2>();
+    float s1[1] = {tm.row_sum(0)};
+    team_sum<1>(s1, tpr, s_red, buf);
+    mean = s1[0] * inv_h;
+  }
   for (; base < rows; base += tm.step) {
     const int64_t t = base + tm.team;
-    tm.fetch(src, t + (kStages - 1) * tm.step, stage == 0 ? kStages - 1 : stage - 1);
-    copy_wait<kStages - 1>();
-    const uint4* ring = tm.mine + stage * tm.stage_vecs;
+    const int after = stage == STAGES - 1 ? 0 : stage + 1;
+    tm.fetch(src, t + (STAGES - 1) * tm.step, stage == 0 ? STAGES - 1 : stage - 1);
+    copy_wait<LAYER ? STAGES - 2 : STAGES - 1>();
+    const uint4* ring = tm.slot(stage);
     // each pass reads the row from shared memory again: registers for 16 more
     // fp32 values would cost the second block of the SM
     auto read = [&](int a, int j) { return ring[(a * VPT + j) * static_cast<int>(blockDim.x)]; };
-    float mean = 0.0f;
-    if (LAYER) {
-      f32x2 acc = 0;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const uint4 xq = read(0, j);
-#pragma unroll
-        for (int i = 0; i < P; ++i) acc = add2(acc, Vec<T>::pair(xq, i));
-      }
-      float s1[1] = {sum2(acc)};
-      team_sum<1>(s1, tpr, s_red, buf);
-      mean = s1[0] * inv_h;
-    }
     const f32x2 neg_mean = pack2(-mean, -mean);
     f32x2 sxx = 0, sgx = 0, sg = 0;       // x'^2, gy x', gy   (x' = x - mean)
 #pragma unroll
@@ -382,11 +418,14 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
           if (LAYER) sg = add2(sg, gy);
         }
       }
-    float s[LAYER ? 3 : 2];
+    float s[LAYER ? 4 : 2];
     s[0] = sum2(sxx);
     s[1] = sum2(sgx);
-    if (LAYER) s[LAYER ? 2 : 0] = sum2(sg);
-    team_sum<LAYER ? 3 : 2>(s, tpr, s_red, buf);
+    if (LAYER) {
+      s[LAYER ? 2 : 0] = sum2(sg);
+      s[LAYER ? 3 : 0] = tm.row_sum(after);
+    }
+    team_sum<LAYER ? 4 : 2>(s, tpr, s_red, buf);
     // dx = r gy - r mean(gy) - k x',  k = r^3 mean(gy x')
     const float r = rsqrtf(s[0] * inv_h + eps);
     const float k = -r * (r * (r * (s[1] * inv_h)));
@@ -413,7 +452,8 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
           }
           dx[t * tm.nv + tm.me + j * tpr] = Vec<T>::put(d);
         }
-    stage = stage == kStages - 1 ? 0 : stage + 1;
+    if (LAYER) mean = s[LAYER ? 3 : 0] * inv_h;
+    stage = after;
   }
   copy_wait<0>();
   // the teams' sums, in order, through shared memory (the ring is done)
@@ -480,32 +520,48 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// out[c] = sum over blocks of part[block][c]: 32 columns a block of threads,
-// warp w adds the partial rows w, w + 32, ... in order, then the warps' sums
-// are added in a fixed tree.
+// out[c] = sum over blocks of part[block][c]: 64 columns a block of threads (so
+// that both gradients of a wide row fit one wave), warp w adds the partial
+// rows w, w + 32, ... in order, then the warps' sums are added in a fixed tree.
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps)
     norm_partials_kernel(const float* __restrict__ part_w, const float* __restrict__ part_b, int blocks,
                          int H, float* __restrict__ dweight, float* __restrict__ dbias) {
-  __shared__ float s_sum[kSumWarps][33];
+  __shared__ float s_sum[kSumWarps][66];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int c = blockIdx.x * 64 + 2 * lane;
   const float* part = blockIdx.y == 0 ? part_w : part_b;
-  float s = 0.0f;
-  if (c < H) {
+  float2 s = make_float2(0.0f, 0.0f);
+  if (H % 2 == 0) {
+    if (c < H) {
 #pragma unroll 4
-    for (int b = warp; b < blocks; b += kSumWarps) s += part[static_cast<int64_t>(b) * H + c];
+      for (int b = warp; b < blocks; b += kSumWarps) {
+        const float2 v = *reinterpret_cast<const float2*>(part + static_cast<int64_t>(b) * H + c);
+        s.x += v.x;
+        s.y += v.y;
+      }
+    }
+  } else {
+    for (int b = warp; b < blocks; b += kSumWarps) {
+      if (c < H) s.x += part[static_cast<int64_t>(b) * H + c];
+      if (c + 1 < H) s.y += part[static_cast<int64_t>(b) * H + c + 1];
+    }
   }
-  s_sum[warp][lane] = s;
+  s_sum[warp][2 * lane] = s.x;
+  s_sum[warp][2 * lane + 1] = s.y;
   __syncthreads();
-  // warp w: column w, over the warps' sums
-  float t = s_sum[lane][warp];
+  // warp w: columns w and w + 32, over the warps' sums
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  const int cw = blockIdx.x * 32 + warp;
-  if (lane == 0 && cw < H) (blockIdx.y == 0 ? dweight : dbias)[cw] = t;
+  for (int half = 0; half < 2; ++half) {
+    const int col = warp + 32 * half;
+    float t = s_sum[lane][col];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    const int cw = blockIdx.x * 64 + col;
+    if (lane == 0 && cw < H) (blockIdx.y == 0 ? dweight : dbias)[cw] = t;
+  }
 }
 
 // Threads of a team and the vectors each holds; 0 vectors: the row has no
@@ -514,20 +570,20 @@ struct TeamShape {
   int vpt, tpr, threads;
   int rows_a_block() const { return threads / tpr; }
 };
-template <typename T> TeamShape team_shape(int H) {
+template <typename T> TeamShape team_shape(int H, bool two_sums) {
   constexpr int V = Vec<T>::V;
   TeamShape s{0, 0, 0};
   if (H % V != 0 || H / V > 4 * kMaxTeam) return s;
   const int nv = H / V;
-  s.vpt = nv <= 32 ? 1 : V == 8 && nv <= 2 * 384 ? 2 : V == 4 && nv <= 64 ? 2 : 4;
+  s.vpt = nv <= 32 || (two_sums && V == 8 && nv <= 768) ? 1 : V == 8 && nv <= 2 * 384 ? 2 : V == 4 && nv <= 64 ? 2 : 4;
   s.tpr = static_cast<int>(ceil_div(ceil_div(nv, s.vpt), 32) * 32);
   const int full = s.vpt == 4 ? 256 : 384;
   s.threads = s.tpr >= full ? s.tpr : full / s.tpr * s.tpr;
   return s;
 }
 // shared memory of a block, and the blocks an SM holds
-size_t ring_bytes(const TeamShape& s, int arrays) {
-  return static_cast<size_t>(kStages) * arrays * s.vpt * s.threads * 16;
+size_t ring_bytes(const TeamShape& s, bool layer, int arrays) {
+  return static_cast<size_t>(stages_of(layer, arrays)) * arrays * s.vpt * s.threads * 16;
 }
 int resident_blocks(int threads_by_regs, const TeamShape& s, size_t smem) {
   return std::max(1, std::min(static_cast<int>(kMaxRing / (smem + 2048)), threads_by_regs / s.threads));
@@ -550,7 +606,7 @@ template <auto Kernel> cudaError_t allow_smem(size_t bytes) {
 template <typename T, int VPT>
 cudaError_t forward_rows(const TeamShape& s, int64_t rows, int H, float eps, const void* x, const void* w,
                          const void* b, void* out, int num_sms, cudaStream_t stream) {
-  const size_t smem = ring_bytes(s, 1);
+  const size_t smem = ring_bytes(s, true, 1);
   const cudaError_t e = allow_smem<layer_norm_rows_kernel<T, VPT>>(smem);
   if (e != cudaSuccess) return e;
   const int64_t groups = ceil_div(rows, s.rows_a_block());
@@ -596,7 +652,7 @@ cudaError_t backward_any(const NormBackwardArgs& a, int blocks, float* part_b, c
 template <typename T>
 cudaError_t forward_of(int64_t rows, int H, float eps, const void* x, const void* w, const void* b, void* out,
                        int num_sms, cudaStream_t stream) {
-  const TeamShape s = team_shape<T>(H);
+  const TeamShape s = team_shape<T>(H, false);
   if (s.vpt == 1) return forward_rows<T, 1>(s, rows, H, eps, x, w, b, out, num_sms, stream);
   if (s.vpt == 2) return forward_rows<T, 2>(s, rows, H, eps, x, w, b, out, num_sms, stream);
   if (s.vpt == 4) return forward_rows<T, 4>(s, rows, H, eps, x, w, b, out, num_sms, stream);
@@ -608,8 +664,8 @@ cudaError_t forward_of(int64_t rows, int H, float eps, const void* x, const void
 // blocks of the partial sums, and the launch that writes them
 template <typename T>
 cudaError_t backward_of(const NormBackwardArgs& a, float* part_b, int num_sms, int* blocks, cudaStream_t stream) {
-  const TeamShape s = team_shape<T>(a.H);
-  const size_t smem = s.vpt == 0 ? 0 : std::max(ring_bytes(s, a.dres != nullptr ? 3 : 2),
+  const TeamShape s = team_shape<T>(a.H, a.layer);
+  const size_t smem = s.vpt == 0 ? 0 : std::max(ring_bytes(s, a.layer, a.dres != nullptr ? 3 : 2),
                                                 static_cast<size_t>(a.H) * sizeof(float));
   const bool team = s.vpt != 0 && smem <= kMaxRing;
   const int64_t groups = team ? ceil_div(a.T, s.rows_a_block()) : a.T;
@@ -637,7 +693,7 @@ cudaError_t launch_norm_backward(const NormBackwardArgs& a, int num_sms, cudaStr
   const cudaError_t e = a.dtype == MOE_BF16 ? backward_of<__nv_bfloat16>(a, part_b, num_sms, &blocks, stream)
                                             : backward_of<float>(a, part_b, num_sms, &blocks, stream);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.H, 32)), a.dbias != nullptr ? 2 : 1);
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.H, 64)), a.dbias != nullptr ? 2 : 1);
   return launch_chained(norm_partials_kernel, grid, dim3(32 * kSumWarps), 0, stream,
                         static_cast<const float*>(a.partials), static_cast<const float*>(part_b), blocks,
                         a.H, a.dweight, a.dbias);
