@@ -13,6 +13,10 @@
 // Backward, for a row of weight w:  s = 1 / (1 + e^-g), a = g s,
 //   dg = w dh u s (1 + g (1 - s)),  du = w dh a,  dw = sum_j dh a u,
 // all in fp32, each output rounded once.
+//
+// Both passes are HBM-bound with little to spare for arithmetic.  A lane takes
+// 8 columns (4 pairs) at a time, so that every load and store of a warp is one
+// run of memory, and four of them are in flight before any is used.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -28,61 +32,81 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlock = 32;      // columns of one scale
 
-template <typename T> __device__ __forceinline__ void load16(const T* p, float (&v)[16]);
-template <> __device__ __forceinline__ void load16<float>(const float* p, float (&v)[16]) {
+// 8 columns (or 4: the h side) of a row as they lie in memory
+template <typename T> struct Cols;
+template <> struct Cols<__nv_bfloat16> {
+  using Eight = uint4;
+  using Four = uint2;
+  __device__ static void get(const uint4& q, float (&v)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = reinterpret_cast<const float4*>(p)[i];
-    v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-  }
-}
-template <> __device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 f = reinterpret_cast<const uint4*>(p)[i];
-    const uint32_t w[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
-}
-template <typename T> __device__ __forceinline__ void store16(T* p, const float (&v)[16]);
-template <> __device__ __forceinline__ void store16<float>(float* p, const float (&v)[16]) {
+  __device__ static void get(const uint2& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x << 16);
+    v[1] = __uint_as_float(q.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(q.y << 16);
+    v[3] = __uint_as_float(q.y & 0xFFFF0000u);
+  }
+  __device__ static uint4 put(const float (&v)[8]) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  }
+  __device__ static uint2 put(const float (&v)[4]) {
+    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  }
+  // largest magnitude as fp32 bits (at or past an infinity's: not finite)
+  __device__ static uint32_t top(const uint4& q, const float (&)[8]) {
+    const uint32_t m = 0x7FFF7FFFu;
+    const uint32_t t = __vmaxu2(__vmaxu2(q.x & m, q.y & m), __vmaxu2(q.z & m, q.w & m));
+    return max(t & 0xFFFF0000u, t << 16);
+  }
+};
+struct alignas(16) F32x8 { float4 a, b; };
+template <> struct Cols<float> {
+  using Eight = F32x8;
+  using Four = float4;
+  __device__ static void get(const F32x8& q, float (&v)[8]) {
+    v[0] = q.a.x; v[1] = q.a.y; v[2] = q.a.z; v[3] = q.a.w;
+    v[4] = q.b.x; v[5] = q.b.y; v[6] = q.b.z; v[7] = q.b.w;
+  }
+  __device__ static void get(const float4& q, float (&v)[4]) { v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w; }
+  __device__ static F32x8 put(const float (&v)[8]) {
+    return F32x8{make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7])};
+  }
+  __device__ static float4 put(const float (&v)[4]) { return make_float4(v[0], v[1], v[2], v[3]); }
+  __device__ static uint32_t top(const F32x8&, const float (&v)[8]) {
+    uint32_t t = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-}
-template <> __device__ __forceinline__ void store16<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    reinterpret_cast<uint4*>(p)[i] =
-        make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                   pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-}
+    for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return t;
+  }
+};
 
 // 2^(b - 127) as fp32 for b in [0, 254]: b = 0 is the subnormal 2^-127
 __device__ __forceinline__ float pow2_of_byte(int b) {
   return __uint_as_float(b > 0 ? static_cast<uint32_t>(b) << 23 : 0x00400000u);
 }
 
-// scale byte of a block whose largest finite magnitude is amax
-__device__ __forceinline__ int scale_byte(float amax) {
-  const uint32_t bits = __float_as_uint(amax);
+// scale byte of a block whose largest finite magnitude has these bits
+__device__ __forceinline__ int scale_byte(uint32_t bits) {
   const int b = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return b > 0 ? b : 0;
 }
 
 __device__ __forceinline__ bool is_finite(float v) { return fabsf(v) <= FLT_MAX; }
 
-// e4m3 bits of two scaled values (|v| <= 448, or not finite: NaN)
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
-  const float2 v = make_float2(is_finite(lo) ? lo * inv : __int_as_float(0x7FC00000),
-                               is_finite(hi) ? hi * inv : __int_as_float(0x7FC00000));
-  return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+// e4m3 bits of 8 finite scaled values (|v inv| <= 448)
+__device__ __forceinline__ uint2 e4m3x8(const float (&v)[8], float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
 // two e4m3 values as fp32 (exact)
@@ -123,113 +147,189 @@ __device__ __forceinline__ int64_t live_rows(const int32_t* live, int64_t rows) 
   return n < 0 ? 0 : (n > rows ? rows : n);
 }
 
-// one thread per block of 32 columns
-template <typename T>
+constexpr int kBatch = 4;       // vectors of 8 columns a thread has in flight
+
+// A team of `lanes` lanes (4..32) or, WIDE, a whole block per row; the 4 lanes
+// that hold a block of 32 columns agree on its scale.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
-    swiglu_checkpoint_kernel(const int32_t* live_ptr, RowWeight rw, int I, const T* __restrict__ gu,
+    swiglu_checkpoint_kernel(const int32_t* live_ptr, RowWeight rw, int I, int lanes, const T* __restrict__ gu,
                              T* __restrict__ h, uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  using C = Cols<T>;
   pdl_wait();
   pdl_trigger();
-  const int nb = I / 16;
-  const int64_t n = live_rows(live_ptr, rw.rows) * nb;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t r = i / nb;
-    const float w = rw.weight(rw.slot(r));
-    float a[16], b[16], out[16];
-    load16(gu + i * kBlock, a);
-    load16(gu + i * kBlock + 16, b);
-    float amax = 0.0f;
+  const int nv = I / 4;                                      // vectors of 8 columns a row
+  const int team_size = WIDE ? kThreads : lanes;
+  const int me = static_cast<int>(threadIdx.x) & (team_size - 1);
+  const int64_t live_n = live_rows(live_ptr, rw.rows);
+  const int teams = kThreads / team_size;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < live_n; base += step) {
+    const int64_t r = base + static_cast<int>(threadIdx.x) / team_size;
+    const bool mine = r < live_n;
+    const float w = mine ? rw.weight(rw.slot(r)) : 0.0f;
+    const int64_t row = (mine ? r : 0) * nv;
+    // every lane of a warp runs the same rounds (the shuffles)
+    for (int vb = 0; vb < nv; vb += kBatch * team_size) {
+      typename C::Eight in[kBatch];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      if (is_finite(a[j])) amax = fmaxf(amax, fabsf(a[j]));
-      if (is_finite(b[j])) amax = fmaxf(amax, fabsf(b[j]));
-    }
-    const int byte = scale_byte(amax);
-    const float inv = pow2_of_byte(254 - byte);
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = vb + b * team_size + me;
+        if (mine && v < nv) in[b] = reinterpret_cast<const typename C::Eight*>(gu)[row + v];
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      out[j] = w * (a[2 * j] * sigmoid(a[2 * j])) * a[2 * j + 1];
-      out[8 + j] = w * (b[2 * j] * sigmoid(b[2 * j])) * b[2 * j + 1];
-    }
-    uint32_t p[8];
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = vb + b * team_size + me;
+        const bool live = mine && v < nv;                    // nv is a multiple of 4: a block's lanes agree
+        float x[8];
+        uint32_t top = 0;
+        if (live) {
+          C::get(in[b], x);
+          top = C::top(in[b], x);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        float out[4];
+        if (live)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      p[j] = e4m3x2(a[4 * j], a[4 * j + 1], inv) | e4m3x2(a[4 * j + 2], a[4 * j + 3], inv) << 16;
-      p[4 + j] = e4m3x2(b[4 * j], b[4 * j + 1], inv) | e4m3x2(b[4 * j + 2], b[4 * j + 3], inv) << 16;
+          for (int j = 0; j < 4; ++j) out[j] = w * (x[2 * j] * sigmoid(x[2 * j])) * x[2 * j + 1];
+        if (__any_sync(0xffffffffu, top >= 0x7F800000u)) {   // rare: the finite values' top, NaN for the others
+          uint32_t t = 0;
+          if (live)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (is_finite(x[j])) t = max(t, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+              else x[j] = __int_as_float(0x7FC00000);        // e4m3 has no infinity
+            }
+          t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          top = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        }
+        if (!live) continue;
+        const int byte = scale_byte(top);
+        reinterpret_cast<typename C::Four*>(h)[row + v] = C::put(out);
+        reinterpret_cast<uint2*>(q)[row + v] = e4m3x8(x, pow2_of_byte(254 - byte));
+        if ((me & 3) == 0) scale[(row + v) >> 2] = static_cast<uint8_t>(byte);
+      }
     }
-    store16(h + i * 16, out);
-    uint4* dst = reinterpret_cast<uint4*>(q + i * kBlock);
-    dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
-    dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
-    scale[i] = static_cast<uint8_t>(byte);
   }
 }
 
-// one warp per row, a block of 32 columns a lane at a time
-template <typename T>
+// A team of `lanes` lanes (4..32) or, WIDE, a whole block per row.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
-    swiglu_backward_kernel(const int32_t* live_ptr, RowWeight rw, int I, const uint8_t* __restrict__ q,
-                           const uint8_t* __restrict__ scale, const T* __restrict__ dh,
-                           T* __restrict__ dgu, float* __restrict__ d_topk_w, T* __restrict__ h) {
+    swiglu_backward_kernel(const int32_t* live_ptr, RowWeight rw, int I, int lanes,
+                           const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                           const T* __restrict__ dh, T* __restrict__ dgu, float* __restrict__ d_topk_w,
+                           T* __restrict__ h) {
+  using C = Cols<T>;
+  __shared__ float s_part[kThreads / 32];
   pdl_wait();
   pdl_trigger();
-  const int nb = I / 16;
-  const int lane = threadIdx.x & 31;
+  const int nv = I / 4;
+  const int team_size = WIDE ? kThreads : lanes;
+  const int me = static_cast<int>(threadIdx.x) & (team_size - 1);
   const int64_t live = live_rows(live_ptr, rw.rows);
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); r < live;
-       r += warps) {
-    const int64_t slot = rw.slot(r);
+  const int teams = kThreads / team_size;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
+  // every lane of a warp runs the same number of rounds (the shuffles below)
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < live; base += step) {
+    const int64_t r = base + static_cast<int>(threadIdx.x) / team_size;
+    const bool mine = r < live;
+    const int64_t slot = mine ? rw.slot(r) : -1;
     const float w = rw.weight(slot);
+    const int64_t row = (mine ? r : 0) * nv;
     float dw = 0.0f;
-    for (int b = lane; b < nb; b += 32) {
-      const int64_t i = r * nb + b;
-      const float s2 = pow2_of_byte(scale[i]);
-      const uint4 q0 = reinterpret_cast<const uint4*>(q + i * kBlock)[0];
-      const uint4 q1 = reinterpret_cast<const uint4*>(q + i * kBlock)[1];
-      const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-      float d[16], o0[16], o1[16], hv[16];
-      load16(dh + i * 16, d);
+    for (int v0 = me; v0 < nv && mine; v0 += kBatch * team_size) {
+      uint2 qv[kBatch];
+      typename C::Four dv[kBatch];
+      uint32_t sb[kBatch];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float2 gu = e4m3x2_f32((qw[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
-        const float g = gu.x * s2, u = gu.y * s2;
-        const float s = sigmoid(g);
-        const float a = g * s;
-        dw = fmaf(d[j], a * u, dw);
-        const float wd = w * d[j];
-        const float dg = wd * u * s * (1.0f + g * (1.0f - s)), du = wd * a;
-        if (j < 8) { o0[2 * j] = dg; o0[2 * j + 1] = du; }
-        else { o1[2 * j - 16] = dg; o1[2 * j - 15] = du; }
-        hv[j] = w * a * u;
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = v0 + b * team_size;
+        if (v >= nv) continue;
+        qv[b] = reinterpret_cast<const uint2*>(q)[row + v];
+        dv[b] = reinterpret_cast<const typename C::Four*>(dh)[row + v];
+        sb[b] = scale[(row + v) >> 2];
       }
-      store16(dgu + i * kBlock, o0);
-      store16(dgu + i * kBlock + 16, o1);
-      if (h != nullptr) store16(h + i * 16, hv);
-    }
-    if (d_topk_w != nullptr) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dw += __shfl_xor_sync(0xffffffffu, dw, o);
-      if (lane == 0 && slot >= 0) d_topk_w[slot] = dw;
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = v0 + b * team_size;
+        if (v >= nv) continue;
+        const float s2 = pow2_of_byte(static_cast<int>(sb[b]));
+        float d[4], o[8], hv[4];
+        C::get(dv[b], d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 gu = e4m3x2_f32(((j < 2 ? qv[b].x : qv[b].y) >> (16 * (j & 1))) & 0xFFFFu);
+          const float g = gu.x * s2, u = gu.y * s2;
+          const float s = sigmoid(g), a = g * s, au = a * u, wd = w * d[j];
+          dw = fmaf(d[j], au, dw);
+          o[2 * j] = wd * u * (s * fmaf(g, 1.0f - s, 1.0f));
+          o[2 * j + 1] = wd * a;
+          hv[j] = w * au;
+        }
+        reinterpret_cast<typename C::Eight*>(dgu)[row + v] = C::put(o);
+        if (h != nullptr) reinterpret_cast<typename C::Four*>(h)[row + v] = C::put(hv);
+      }
     }
+    if (d_topk_w == nullptr) continue;                       // uniform
+    for (int o = min(team_size, 32) >> 1; o > 0; o >>= 1) dw += __shfl_xor_sync(0xffffffffu, dw, o);
+    if (WIDE) {
+      if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = dw;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        dw = 0.0f;
+        for (int i = 0; i < kThreads / 32; ++i) dw += s_part[i];
+      }
+      __syncthreads();
+    }
+    if (me == 0 && slot >= 0) d_topk_w[slot] = dw;
   }
+}
+
+// The fewest lanes (4..32) that cover a row; with too few rows for that many
+// teams, and long ones, a block per row.
+struct TeamShape {
+  int lanes;
+  bool wide;
+  unsigned grid;
+};
+TeamShape team_shape(const SwigluArgs& a, int num_sms) {
+  TeamShape s{4, false, 1};
+  const int nv = a.I / 4;
+  while (s.lanes < nv && s.lanes < 32) s.lanes <<= 1;
+  s.wide = nv >= 2 * kThreads / kBatch && a.rows < static_cast<int64_t>(num_sms) * 16;
+  const int64_t blocks = s.wide ? a.rows : ceil_div(a.rows, kThreads / s.lanes);
+  s.grid = static_cast<unsigned>(std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * 16));
+  return s;
+}
+
+template <typename T>
+cudaError_t checkpoint_of(const SwigluArgs& a, const void* gu, void* h, void* q, uint8_t* scale, int num_sms,
+                          cudaStream_t stream) {
+  const RowWeight rw{a.perm_slot, a.topk_w, a.rows, a.status};
+  const TeamShape s = team_shape(a, num_sms);
+  return launch_chained(s.wide ? swiglu_checkpoint_kernel<T, true> : swiglu_checkpoint_kernel<T, false>, s.grid,
+                        kThreads, 0, stream, a.live, rw, a.I, s.lanes, static_cast<const T*>(gu),
+                        static_cast<T*>(h), static_cast<uint8_t*>(q), scale);
+}
+
+template <typename T>
+cudaError_t backward_of(const SwigluArgs& a, const void* q, const uint8_t* scale, const void* dh, void* dgu,
+                        float* d_topk_w, void* h, int num_sms, cudaStream_t stream) {
+  const RowWeight rw{a.perm_slot, a.topk_w, a.rows, a.status};
+  const TeamShape s = team_shape(a, num_sms);
+  return launch_chained(s.wide ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>, s.grid,
+                        kThreads, 0, stream, a.live, rw, a.I, s.lanes, static_cast<const uint8_t*>(q), scale,
+                        static_cast<const T*>(dh), static_cast<T*>(dgu), d_topk_w, static_cast<T*>(h));
 }
 
 }  // namespace
 
 cudaError_t launch_swiglu_checkpoint(const SwigluArgs& a, const void* gu, void* h, void* q,
                                      uint8_t* scale, int num_sms, cudaStream_t stream) {
-  const RowWeight rw{a.perm_slot, a.topk_w, a.rows, a.status};
-  const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>(ceil_div(a.rows * (a.I / 16), kThreads), static_cast<int64_t>(num_sms) * 8));
-  if (a.dtype == MOE_BF16)
-    return launch_chained(swiglu_checkpoint_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, a.live,
-                          rw, a.I, static_cast<const __nv_bfloat16*>(gu),
-                          static_cast<__nv_bfloat16*>(h), static_cast<uint8_t*>(q), scale);
-  return launch_chained(swiglu_checkpoint_kernel<float>, grid, kThreads, 0, stream, a.live, rw, a.I,
-                        static_cast<const float*>(gu), static_cast<float*>(h),
-                        static_cast<uint8_t*>(q), scale);
+  return a.dtype == MOE_BF16 ? checkpoint_of<__nv_bfloat16>(a, gu, h, q, scale, num_sms, stream)
+                             : checkpoint_of<float>(a, gu, h, q, scale, num_sms, stream);
 }
 
 cudaError_t launch_swiglu_backward(const SwigluArgs& a, const void* q, const uint8_t* scale,
@@ -241,17 +341,8 @@ cudaError_t launch_swiglu_backward(const SwigluArgs& a, const void* q, const uin
     const cudaError_t e = cudaMemsetAsync(d_topk_w, 0, static_cast<size_t>(a.rows) * 4, stream);
     if (e != cudaSuccess) return e;
   }
-  const RowWeight rw{a.perm_slot, a.topk_w, a.rows, a.status};
-  const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>(ceil_div(a.rows, kThreads / 32), static_cast<int64_t>(num_sms) * 8));
-  const uint8_t* qb = static_cast<const uint8_t*>(q);
-  if (a.dtype == MOE_BF16)
-    return launch_chained(swiglu_backward_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, a.live, rw,
-                          a.I, qb, scale, static_cast<const __nv_bfloat16*>(dh),
-                          static_cast<__nv_bfloat16*>(dgu), d_topk_w, static_cast<__nv_bfloat16*>(h));
-  return launch_chained(swiglu_backward_kernel<float>, grid, kThreads, 0, stream, a.live, rw, a.I, qb,
-                        scale, static_cast<const float*>(dh), static_cast<float*>(dgu), d_topk_w,
-                        static_cast<float*>(h));
+  return a.dtype == MOE_BF16 ? backward_of<__nv_bfloat16>(a, q, scale, dh, dgu, d_topk_w, h, num_sms, stream)
+                             : backward_of<float>(a, q, scale, dh, dgu, d_topk_w, h, num_sms, stream);
 }
 
 }  // namespace moe
