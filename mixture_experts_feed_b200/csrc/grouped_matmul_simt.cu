@@ -7,9 +7,14 @@
 //   dgrad    P = dout [R, n] (r contiguous), Q = W[e]        (j contiguous)
 //   wgrad    P = dout        (i contiguous), Q = a           (j contiguous)
 //
-// Tiles of 64 x 64 outputs, 16 of r at a time through shared memory, 256
-// threads with 4 x 4 outputs each.  The reduction runs in one fixed order, so
-// results repeat bit for bit.
+// Tiles of TB x TB outputs, 16 of r at a time through shared memory in two
+// buffers (the next step's operands are in flight while this one is used), 256
+// threads with (TB / 16)^2 outputs each.  TB = 128 reads 64 bytes of shared
+// memory for 64 FMAs a thread and step, TB = 64 32 bytes for 16: the larger
+// tile where its tiles fill the SMs, the smaller one elsewhere.  Products
+// go two at a time (packed fp32 FMAs): the same rate from the FMA pipe for half
+// the issue slots, which the loads need.  The reduction
+// runs in one fixed order, so results repeat bit for bit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,7 +29,7 @@
 namespace moe {
 namespace {
 
-constexpr int TB = 64, TR = 16, NT = 256;
+constexpr int TR = 16, NT = 256;
 
 __device__ __forceinline__ float elem_f32(float v) { return v; }
 __device__ __forceinline__ float elem_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -34,28 +39,63 @@ template <> __device__ __forceinline__ float elem_from<float>(float v) { return 
 template <> __device__ __forceinline__ __nv_bfloat16 elem_from<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half elem_from<__half>(float v) { return __float2half_rn(v); }
 
-// tile[r][x] = M[x0 + x, r0 + r], zero outside nx x nr.  RED: r contiguous
-// (element x * ld + r), else x contiguous (r * ld + x).
-template <bool RED, typename T>
-__device__ __forceinline__ void load_tile(const T* __restrict__ m, int64_t ld, int64_t x0, int64_t nx,
-                                          int64_t r0, int64_t nr, float (*tile)[TB + 4]) {
-  const int tid = threadIdx.x;
-  if (RED) {
-    const int x = tid >> 2, r = (tid & 3) * 4;
-    const bool ok = x0 + x < nx;
-    const T* src = m + (ok ? (x0 + x) * ld : 0) + r0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      tile[r + q][x] = ok && r0 + r + q < nr ? elem_f32(src[r + q]) : 0.0f;
-  } else {
-    const int r = tid >> 4, x = (tid & 15) * 4;
-    const bool ok = r0 + r < nr;
-    const T* src = m + (ok ? (r0 + r) * ld : 0) + x0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      tile[r][x + q] = ok && x0 + x + q < nx ? elem_f32(src[x + q]) : 0.0f;
-  }
+// Four consecutive elements; `vec`: 16-byte (fp32) or 8-byte aligned.
+template <typename T> __device__ __forceinline__ float4 load4(const T* p) {
+  const uint2 q = *reinterpret_cast<const uint2*>(p);
+  const T* t = reinterpret_cast<const T*>(&q);
+  return make_float4(elem_f32(t[0]), elem_f32(t[1]), elem_f32(t[2]), elem_f32(t[3]));
 }
+template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
+// One operand's tile of TB x TR, as M[x0 + x, r0 + r] with zeros outside
+// nx x nr.  RED: r contiguous (element x * ld + r), else x contiguous
+// (r * ld + x).  A thread carries TB / 64 groups of 4 elements from global
+// memory (fetch) to shared memory (place: tile[r][x]).
+template <bool RED, int TB, typename T> struct Operand {
+  static constexpr int G = TB / 64;
+  const T* m;
+  int64_t ld, x0, nx, nr;
+  bool vec;
+  float4 v[G];
+  __device__ __forceinline__ void where(int g, int& x, int& r) const {
+    const int i = static_cast<int>(threadIdx.x) + g * NT;
+    x = RED ? i >> 2 : (i % (TB / 4)) * 4;
+    r = RED ? (i & 3) * 4 : i / (TB / 4);
+  }
+  __device__ __forceinline__ void fetch(int64_t r0) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      int x, r;
+      where(g, x, r);
+      const int64_t xx = x0 + x, rr = r0 + r;
+      const int64_t left = RED ? (xx < nx ? nr - rr : 0) : (rr < nr ? nx - xx : 0);   // of the 4
+      const T* p = m + (RED ? xx * ld + rr : rr * ld + xx);
+      if (left >= 4 && vec) {
+        v[g] = load4(p);
+      } else {
+        v[g].x = left > 0 ? elem_f32(p[0]) : 0.0f;
+        v[g].y = left > 1 ? elem_f32(p[1]) : 0.0f;
+        v[g].z = left > 2 ? elem_f32(p[2]) : 0.0f;
+        v[g].w = left > 3 ? elem_f32(p[3]) : 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void place(float (*tile)[TB + 4]) const {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      int x, r;
+      where(g, x, r);
+      if (RED) {
+        tile[r][x] = v[g].x;
+        tile[r + 1][x] = v[g].y;
+        tile[r + 2][x] = v[g].z;
+        tile[r + 3][x] = v[g].w;
+      } else {
+        *reinterpret_cast<float4*>(&tile[r][x]) = v[g];
+      }
+    }
+  }
+};
 
 struct SimtProduct {
   const void *p, *q;
@@ -63,12 +103,14 @@ struct SimtProduct {
   const int32_t* offsets;
   int32_t* status;
   int E, n, k, rows_cap, accumulate;
+  int vec_p, vec_q;      // rows of whole 4-element vectors
 };
 
-template <int FORM, typename T, typename O>
-__global__ void __launch_bounds__(NT) grouped_matmul_simt_kernel(const SimtProduct g) {
-  __shared__ __align__(16) float Ps[TR][TB + 4];
-  __shared__ __align__(16) float Qs[TR][TB + 4];
+template <int FORM, int TB, typename T, typename O>
+__global__ void __launch_bounds__(NT, TB == 64 ? 3 : 2) grouped_matmul_simt_kernel(const SimtProduct g) {
+  constexpr int M = TB / 16;             // outputs a thread, each way
+  __shared__ __align__(16) float Ps[2][TR][TB + 4];
+  __shared__ __align__(16) float Qs[2][TR][TB + 4];
   __shared__ int s_bad;
   extern __shared__ int s_tables[];
   int* s_off = s_tables;
@@ -114,38 +156,66 @@ __global__ void __launch_bounds__(NT) grouped_matmul_simt_kernel(const SimtProdu
       P += row0 * (FORM == kForward ? g.k : g.n);
       Q += static_cast<int64_t>(e) * g.n * g.k;
     }
-    float acc[4][4];
+    f32x2 acc[M][M / 2];                 // neighbouring columns as packed pairs
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int a = 0; a < M; ++a)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) acc[a][b] = 0.0f;
-    for (int64_t r0 = 0; r0 < nr; r0 += TR) {
-      load_tile<FORM != kWgrad>(P, FORM == kForward ? g.k : g.n, i0, ni, r0, nr, Ps);
-      load_tile<FORM == kForward>(Q, g.k, j0, cols, r0, nr, Qs);
+      for (int b = 0; b < M / 2; ++b) acc[a][b] = 0;
+    Operand<FORM != kWgrad, TB, T> op{P, FORM == kForward ? g.k : g.n, i0, ni, nr, g.vec_p != 0};
+    Operand<FORM == kForward, TB, T> oq{Q, g.k, j0, cols, nr, g.vec_q != 0};
+    int buf = 0;
+    __syncthreads();                     // the previous tile's last buffer is free
+    if (nr > 0) {
+      op.fetch(0);
+      oq.fetch(0);
+      op.place(Ps[0]);
+      oq.place(Qs[0]);
       __syncthreads();
+    }
+    for (int64_t r0 = 0; r0 < nr; r0 += TR) {
+      const bool more = r0 + TR < nr;
+      if (more) {
+        op.fetch(r0 + TR);
+        oq.fetch(r0 + TR);
+      }
 #pragma unroll
       for (int r = 0; r < TR; ++r) {
-        const float4 pv = *reinterpret_cast<const float4*>(&Ps[r][ty * 4]);
-        const float4 qv = *reinterpret_cast<const float4*>(&Qs[r][tx * 4]);
-        const float pa[4] = {pv.x, pv.y, pv.z, pv.w}, qa[4] = {qv.x, qv.y, qv.z, qv.w};
+        float pa[M];
+        f32x2 qa[M / 2];
+        // thread (ty, tx) holds rows 4 ty + 64 h.. and columns 4 tx + 64 h..
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
+        for (int h = 0; h < M / 4; ++h) {
+          const float4 pv = *reinterpret_cast<const float4*>(&Ps[buf][r][ty * 4 + 64 * h]);
+          const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(&Qs[buf][r][tx * 4 + 64 * h]);
+          pa[4 * h] = pv.x; pa[4 * h + 1] = pv.y; pa[4 * h + 2] = pv.z; pa[4 * h + 3] = pv.w;
+          qa[2 * h] = qv.x; qa[2 * h + 1] = qv.y;
+        }
 #pragma unroll
-          for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(pa[a], qa[b], acc[a][b]);
+        for (int a = 0; a < M; ++a) {
+          const f32x2 p2 = pack2(pa[a], pa[a]);
+#pragma unroll
+          for (int b = 0; b < M / 2; ++b) acc[a][b] = fma2(p2, qa[b], acc[a][b]);
+        }
       }
-      __syncthreads();
+      if (more) {
+        op.place(Ps[buf ^ 1]);
+        oq.place(Qs[buf ^ 1]);
+        __syncthreads();
+        buf ^= 1;
+      }
     }
     O* out = static_cast<O*>(g.out) + (FORM == kWgrad ? static_cast<int64_t>(e) * g.n : row0) * cols;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int64_t i = i0 + ty * 4 + a;
+    for (int a = 0; a < M; ++a) {
+      const int64_t i = i0 + ty * 4 + 64 * (a / 4) + a % 4;
       if (i >= ni) continue;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int64_t j = j0 + tx * 4 + b;
+      for (int b = 0; b < M; ++b) {
+        const int64_t j = j0 + tx * 4 + 64 * (b / 4) + b % 4;
         if (j >= cols) continue;
         O* dst = out + i * cols + j;
-        float v = acc[a][b];
+        const float2 pr = unpack2(acc[a][b / 2]);
+        float v = b % 2 == 0 ? pr.x : pr.y;
         if (FORM == kWgrad && g.accumulate) v += elem_f32(*dst);
         *dst = elem_from<O>(v);
       }
@@ -153,18 +223,31 @@ __global__ void __launch_bounds__(NT) grouped_matmul_simt_kernel(const SimtProdu
   }
 }
 
+// tiles of TB x TB at most (each group may end in a partial row tile)
+template <int FORM> int64_t tile_bound(const GroupedProduct& g, int tb) {
+  const int64_t j_tiles = ceil_div(FORM == kForward ? g.n : g.k, tb);
+  return FORM == kWgrad ? g.E * ceil_div(g.n, tb) * j_tiles : (ceil_div(g.rows, tb) + g.E) * j_tiles;
+}
+
+template <int FORM, int TB, typename T, typename O>
+cudaError_t launch_tile(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
+  SimtProduct s{g.p, g.q, g.out, g.offsets, g.status, g.E, g.n, g.k, static_cast<int>(g.rows), g.accumulate, 0, 0};
+  // rows start on vector boundaries (the operands are 16-byte aligned)
+  s.vec_p = (FORM == kForward ? g.k : g.n) % 4 == 0;
+  s.vec_q = g.k % 4 == 0;
+  const size_t smem = sizeof(int) * (2 * static_cast<size_t>(g.E) + 2);
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(
+      1, std::min<int64_t>(tile_bound<FORM>(g, TB), static_cast<int64_t>(num_sms) * (TB == 64 ? 4 : 2))));
+  return launch_chained(grouped_matmul_simt_kernel<FORM, TB, T, O>, grid, NT, smem, stream, s);
+}
+
 template <int FORM, typename T, typename O>
 cudaError_t launch_form(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
-  SimtProduct s{g.p, g.q, g.out, g.offsets, g.status, g.E, g.n, g.k, static_cast<int>(g.rows), g.accumulate};
-  const size_t smem = sizeof(int) * (2 * static_cast<size_t>(g.E) + 2);
-  const int cols = FORM == kForward ? g.n : g.k;
-  const int64_t j_tiles = ceil_div(cols, TB);
-  // at most this many tiles (each group may end in a partial row tile)
-  const int64_t tiles = FORM == kWgrad ? g.E * ceil_div(g.n, TB) * j_tiles
-                                       : (ceil_div(g.rows, TB) + g.E) * j_tiles;
-  const unsigned grid = static_cast<unsigned>(
-      std::max<int64_t>(1, std::min<int64_t>(tiles, static_cast<int64_t>(num_sms) * 4)));
-  return launch_chained(grouped_matmul_simt_kernel<FORM, T, O>, grid, NT, smem, stream, s);
+  // rows / 128 + E bounds the tiles from above by E: full tiles alone count
+  const int64_t full = FORM == kWgrad ? tile_bound<FORM>(g, 128)
+                                      : g.rows / 128 * ceil_div(FORM == kForward ? g.n : g.k, 128);
+  return full >= num_sms ? launch_tile<FORM, 128, T, O>(g, num_sms, stream)
+                         : launch_tile<FORM, 64, T, O>(g, num_sms, stream);
 }
 
 template <typename T, typename O>
