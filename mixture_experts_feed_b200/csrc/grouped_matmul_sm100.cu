@@ -66,7 +66,7 @@ constexpr int EPI_WARPS = 8;              // two per quarter of the tensor memor
 constexpr int SCHED_WARP = 2 + EPI_WARPS;
 constexpr int FIX_WARP = SCHED_WARP + 1; // wgrad's last blocks
 __host__ __device__ constexpr int num_threads(int form) { return 32 * (form == kWgrad ? FIX_WARP + 1 : FIX_WARP); }
-constexpr int OUT_BYTES = 4096;          // an epilogue warp's staging: 32 j x 64 i (16-bit) or x 32 i (fp32)
+constexpr int OUT_BYTES = 4096;          // staging of an epilogue warp (16-bit: 8 KB for two warps)
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
 constexpr int TQ = 8;                    // slots of the tile queue
 constexpr int kBand = 8;                 // i tiles per band (tile order)
@@ -76,8 +76,8 @@ constexpr int kMaxSmem = 232448;         // shared memory a block can have
 struct alignas(64) ProductParams {
   CUtensorMap tmM;       // M side
   CUtensorMap tmN[4];    // N side: boxes of 128, 64, 32 and 16 rows (wgrad: [0] alone)
-  CUtensorMap tmOut;     // output [depth][i][j]: boxes of 32 j x 64 i (16-bit) or 32 i (fp32)
-  CUtensorMap tmOut32;   // 16-bit: boxes of 32 j x 32 i
+  CUtensorMap tmOut;     // output [depth][i][j]: boxes of 64 j x 64 i (16-bit) or 32 x 32 (fp32)
+  CUtensorMap tmOut32;   // 16-bit: boxes of 64 j x 32 i
   const int32_t* offsets;
   int32_t* status;
   void* out;
@@ -89,8 +89,8 @@ struct alignas(64) ProductParams {
 };
 
 struct Smem {
-  // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain, tq[TQ], tqe[TQ]
-  static constexpr int kNumBars = 3 * STAGES + 5 + 2 * TQ;
+  // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain, tq[TQ], tqe[TQ], pair[4]
+  static constexpr int kNumBars = 3 * STAGES + 9 + 2 * TQ;
   // the stages, 4 KB of staging a warp, the tile queue, the barriers, then
   // tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
   static constexpr int kFixed = TQ * 32 + kNumBars * 8 + 16;
@@ -251,55 +251,69 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, got);
 }
 
-// An epilogue warp stages 4 KB at a time ([i][32 j]: 16-bit 64 rows of 64
-// bytes, fp32 32 rows of 128) and hands it to TMA (flush).  The buffer is free
-// again once the store has read it.
-__device__ __forceinline__ void stage_free() {
-  if (elect_one()) bulk_wait_group_read0();
-  __syncwarp();
-}
+// Staging of the outputs.  fp32: each epilogue warp stages 32 i x 32 j (rows of
+// 128 bytes).  16-bit: two warps of neighbouring quarters stage 64 i x 64 j
+// together, so that rows are 128 bytes there too: the TMA unit, which also
+// brings the operands, spends as long on a row of 64 bytes as on one of 128.
+// The buffer is free again once the store that used it last has read it.
+struct OutStage {
+  uint8_t* buf;
+  uint64_t* bar;          // 16-bit: the two warps' barrier
+  uint32_t phase;
+  bool issuer;            // this warp hands the buffer to TMA
+  volatile int* abort;
+  int32_t* status;
+  // both warps of a 16-bit buffer; false after a timeout (nothing is left waiting)
+  __device__ __forceinline__ bool pair_sync() {
+    __syncwarp();
+    if (elect_one()) mbar_arrive(bar);
+    const bool ok = all_wait(bar, phase, abort, status);
+    phase ^= 1u;
+    return ok;
+  }
+};
 
-// Byte offset of 16-byte piece c of row r of the staging: 16-bit rows carry
-// TMA's 64-byte swizzle, which spreads the 8 rows a transposing store writes
+// Byte offset of 16-byte piece c of row r of the staging: 16-bit buffers carry
+// TMA's 128-byte swizzle, which spreads the 8 rows a transposing store writes
 // at once over all banks.
 template <int ELEM> __device__ __forceinline__ int box_piece(int r, int c) {
-  return ELEM == 4 ? r * 128 + c * 16 : r * 64 + ((c ^ ((r >> 1) & 3)) * 16);
+  return r * 128 + (ELEM == 4 ? c : c ^ (r & 7)) * 16;
 }
 
 // The staged rows to out rows row.. at column j; `left` of them count (a
 // multiple of 32 except at the end of i).  Whole boxes go by TMA, which clips
 // at the edges of the output matrix (wgrad: of the expert's matrix); a
 // group's last rows are stored by the threads, since a box would write the
-// next group's rows.
+// next group's rows.  The staged values are visible to TMA and to the threads.
 template <int FORM, int ELEM>
-__device__ __forceinline__ void flush(const ProductParams& p, const uint8_t* buf, int j, int row, int depth,
+__device__ __forceinline__ void flush(const ProductParams& p, const OutStage& os, int j, int row, int depth,
                                       int left, int lane) {
-  constexpr int ROWS = 128 / ELEM, PIECES = 32 * ELEM / 16;            // 16-byte pieces a row
-  fence_proxy_async_smem();
-  __syncwarp();
+  constexpr int ROWS = ELEM == 4 ? 32 : 64;
   int done = 0;                                                        // rows that TMA takes
   if (left >= ROWS || (FORM == kWgrad && left > ROWS - 32)) {
     done = ROWS;
-    if (elect_one()) {
-      if (FORM == kWgrad && ELEM == 4 && p.accumulate) tma_add_3d(&p.tmOut, buf, j, row, depth);
-      else tma_store_3d(&p.tmOut, buf, j, row, depth);
+    if (os.issuer && elect_one()) {
+      if (FORM == kWgrad && ELEM == 4 && p.accumulate) tma_add_3d(&p.tmOut, os.buf, j, row, depth);
+      else tma_store_3d(&p.tmOut, os.buf, j, row, depth);
       bulk_commit_group();
     }
   } else if (ELEM == 2 && (FORM == kWgrad || left >= 32)) {
     done = 32;
-    if (elect_one()) {
-      tma_store_3d(&p.tmOut32, buf, j, row, depth);
+    if (os.issuer && elect_one()) {
+      tma_store_3d(&p.tmOut32, os.buf, j, row, depth);
       bulk_commit_group();
     }
   }
   if (FORM != kWgrad && done < left && done < ROWS) {
+    // 8 pieces of 16 bytes a row; two warps take every other run of 32
+    const int first = ELEM == 4 || os.issuer ? 0 : 32, step = ELEM == 4 ? 32 : 64;
 #pragma unroll 1
-    for (int x = done * PIECES + lane; x < left * PIECES; x += 32) {
-      const int r = x / PIECES, c = x % PIECES, jj = j + c * (16 / ELEM);
+    for (int x = done * 8 + first + lane; x < left * 8; x += step) {
+      const int r = x >> 3, c = x & 7, jj = j + c * (16 / ELEM);
       if (jj < p.n_j)
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
                                   (static_cast<int64_t>(row + r) * p.n_j + jj) * ELEM) =
-            *reinterpret_cast<const uint4*>(buf + box_piece<ELEM>(r, c));
+            *reinterpret_cast<const uint4*>(os.buf + box_piece<ELEM>(r, c));
     }
   }
   __syncwarp();
@@ -329,6 +343,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
   uint64_t* drain = tempty + 2;
   uint64_t* tq = drain + 1;              // a tile is in the queue; its readers have it
   uint64_t* tqe = tq + TQ;
+  uint64_t* pair = tqe + TQ;             // 16-bit staging: its two warps
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + Smem::kNumBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
@@ -358,6 +373,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         mbar_init(&tempty[i], 2 * EPI_WARPS);   // the epilogue warps of both CTAs
       }
       mbar_init(drain, 1);
+      for (int i = 0; i < 4; ++i) mbar_init(&pair[i], 2);
       for (int i = 0; i < TQ; ++i) {
         mbar_init(&tq[i], 1);
         // the producer and the epilogue warps; rank 0's issuer; wgrad's FIX_WARP
@@ -606,9 +622,12 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
     // 64 (fp32: 32) columns (i).
     const int quarter = warp & 3, part = (warp - 2) >> 2;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* st = ring_end + (warp - 2) * OUT_BYTES;
+    const int sharing = part * 2 + (quarter >> 1);         // 16-bit: this warp's buffer
+    OutStage os{ring_end + (F32 ? (warp - 2) * OUT_BYTES : sharing * 2 * OUT_BYTES), &pair[sharing], 0,
+                F32 || (quarter & 1) == 0, s_abort, p.status};
     // transposing stores: lane 8m + r gives row r of an 8-row group, piece m
-    const uint32_t st_addr = smem_u32(st) + static_cast<uint32_t>(box_piece<2>(lane & 7, lane >> 3));
+    const uint32_t st_addr =
+        smem_u32(os.buf) + static_cast<uint32_t>(box_piece<2>(lane & 7, (quarter & 1) * 4 + (lane >> 3)));
     int it = 0;
     bool ok = true;
     TileInfo t;
@@ -650,10 +669,13 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
           for (int x = 0; x < 4; ++x) {
             const int c = (2 * x + part) * 32;
             if (c < t.ni) {
-              stage_free();
+              if (elect_one()) bulk_wait_group_read0();
+              __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(st + i * 128 + lane * 4) = sum[x][i];
-              flush<FORM, 4>(p, st, j, row + c, depth, t.ni - c, lane);
+              for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(os.buf + i * 128 + lane * 4) = sum[x][i];
+              fence_proxy_async_smem();
+              __syncwarp();
+              flush<FORM, 4>(p, os, j, row + c, depth, t.ni - c, lane);
             }
           }
         }
@@ -661,7 +683,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         // 64 columns at a time: 8 x 8 fragments, rounded in pairs and stored
         // transposed
         const int acc = it & 1;
-        if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) break;
+        if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
         tc_fence_after();
         auto release = [&] {                               // to the issuer's barrier
           tc_fence_before();
@@ -685,7 +707,8 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
             for (int i = 0; i < 64; ++i) v[i] = 0;
           }
           if (c + 128 >= t.ni) release();                  // this warp's last columns are in registers
-          if (j < p.n_j) {                                 // warp-uniform
+          const int j_box = j & ~63;                       // both warps' 64 columns
+          if (j_box < p.n_j) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -697,15 +720,18 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
                 w[i] = pack_bf16x2(lo, hi);
               }
             }
-            stage_free();
+            if (os.issuer && elect_one()) bulk_wait_group_read0();
+            if (!os.pair_sync()) { ok = false; break; }
             // w[16 h16 + 8 half + 2 n + h8]: j 16 h16 + 8 h8 .., i 32 half + 8 n ..
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
               for (int n = 0; n < 4; ++n)
-                stmatrix_x4_trans(st_addr + half * 2048 + n * 512, w[8 * half + 2 * n], w[8 * half + 2 * n + 1],
+                stmatrix_x4_trans(st_addr + half * 4096 + n * 1024, w[8 * half + 2 * n], w[8 * half + 2 * n + 1],
                                   w[16 + 8 * half + 2 * n], w[16 + 8 * half + 2 * n + 1]);
-            flush<FORM, 2>(p, st, j, row + c, depth, t.ni - c, lane);
+            fence_proxy_async_smem();
+            if (!os.pair_sync()) { ok = false; break; }
+            flush<FORM, 2>(p, os, j_box, row + c, depth, t.ni - c, lane);
           }
         }
         if (part * 64 >= t.ni) release();                  // no columns of its own
@@ -757,7 +783,7 @@ bool encode(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t ro
                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return fn(m, type, depth > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-            swizzle == CU_TENSOR_MAP_SWIZZLE_128B ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -822,7 +848,7 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
   p.fmt = f16 ? 0u : (1u << 7) | (1u << 10);
   const int64_t rows = g.rows > 0 ? g.rows : 1;   // wgrad of no rows: maps are never read
   const CUtensorMapSwizzle kIn = CU_TENSOR_MAP_SWIZZLE_128B;
-  const CUtensorMapSwizzle kOut = f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle kOut = f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
   bool ok;
   int64_t max_tiles;
   if (g.form == kWgrad) {
@@ -831,8 +857,8 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     const void* any = g.rows > 0 ? g.q : g.out;
     ok = encode(&p.tmM, any, g.dtype, g.k, rows, 0, BK, BK, kIn) &&
          encode(&p.tmN[0], g.rows > 0 ? g.p : g.out, g.dtype, g.n, rows, 0, BK, BK, kIn) &&
-         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, 32, f32 ? 32 : 64, kOut) &&
-         encode(&p.tmOut32, g.out, g.out_dtype, g.k, g.n, g.E, 32, 32, kOut);
+         encode(&p.tmOut, g.out, g.out_dtype, g.k, g.n, g.E, f32 ? 32 : 64, f32 ? 32 : 64, kOut) &&
+         encode(&p.tmOut32, g.out, g.out_dtype, g.k, g.n, g.E, f32 ? 32 : 64, 32, kOut);
     p.tmN[1] = p.tmN[2] = p.tmN[3] = p.tmN[0];
     max_tiles = static_cast<int64_t>(g.E) * tiles_over(g.n, TN) * tiles_over(g.k, TM);
   } else {
@@ -841,8 +867,8 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
     p.n_r = red;
     // forward: boxes of 64 k x 128 n; dgrad: 64 k x 64 n (k is j)
     ok = encode(&p.tmM, g.q, g.dtype, g.k, g.n, g.E, BK, g.form == kForward ? 128 : BK, kIn) &&
-         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, f32 ? 32 : 64, kOut) &&
-         encode(&p.tmOut32, g.out, g.out_dtype, p.n_j, g.rows, 1, 32, 32, kOut);
+         encode(&p.tmOut, g.out, g.out_dtype, p.n_j, g.rows, 1, f32 ? 32 : 64, f32 ? 32 : 64, kOut) &&
+         encode(&p.tmOut32, g.out, g.out_dtype, p.n_j, g.rows, 1, f32 ? 32 : 64, 32, kOut);
     for (int x = 0; x < 4; ++x)
       ok = ok && encode(&p.tmN[x], g.p, g.dtype, red, rows, 0, BK, 128 >> x, kIn);
     max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
