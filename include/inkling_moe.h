@@ -505,8 +505,9 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* 
  * Offsets that decrease or leave [0, R] are recorded in the status word
  * (MOE_ERR_DEVICE_CHECK) and read as the nearest valid ones.
  * bf16 and fp16 operands with n % 8 == 0 and k % 8 == 0 run on the tensor
- * cores; fp32 operands and other sizes on the CUDA cores.  Outputs must not
- * overlap operands.  R = 0: the first two launch nothing; the third still
+ * cores (one launch for all experts); fp32 operands and other sizes on the
+ * CUDA cores.  An fp16 output past 65504 becomes an infinity.  Outputs must
+ * not overlap operands.  R = 0: the first two launch nothing; the third still
  * reads expert_offsets and writes dW.
  */
 moe_status_t moe_grouped_matmul(const moe_grouped_desc_t* desc, const void* a, const void* w,
@@ -538,8 +539,9 @@ moe_status_t moe_grouped_matmul_wgrad(const moe_grouped_desc_t* desc, const void
  *              expert_offsets[n_groups] are left alone; NULL: all R rows.
  * dtype MOE_F32 or MOE_BF16; I % 16 == 0 (else MOE_ERR_UNSUPPORTED);
  * perm_slot and topk_w have R entries.  A slot outside [0, R) is recorded in
- * the status word and its row takes weight 0.  workspace: at least 256 bytes
- * whose head is an initialised status word.
+ * the status word and its row takes weight 0.  Outputs must not overlap
+ * inputs.  workspace: at least 256 bytes whose head is an initialised status
+ * word.
  */
 moe_status_t moe_swiglu_checkpoint(int64_t rows, int32_t intermediate, moe_dtype_t dtype,
                                    const void* gu, int32_t n_groups, const int32_t* expert_offsets,
@@ -558,7 +560,7 @@ moe_status_t moe_swiglu_checkpoint(int64_t rows, int32_t intermediate, moe_dtype
  *                       activation again, for the down product's weight
  *                       gradient, so that the forward need not keep it)
  *   dh [R, I] dtype; the other arguments as above.  perm_slot must not hold
- * a slot twice (moe_permute's does not).
+ * a slot twice (moe_permute's does not).  Outputs must not overlap inputs.
  */
 moe_status_t moe_swiglu_backward(int64_t rows, int32_t intermediate, moe_dtype_t dtype,
                                  const void* q, const uint8_t* scale, const void* dh,
@@ -591,7 +593,9 @@ moe_status_t moe_norm_workspace_size(int64_t num_tokens, int32_t hidden, size_t*
  *             mean(gy)); dres [T, H] (the residual path's gradient) or NULL
  *   dweight = sum_t dout x^,  dbias = sum_t dout    [H] fp32, in a fixed order
  * x, dout, dres, dx [T, H] and weight [H] in `dtype`; dbias may be NULL.
- * dx may equal dout or dres.  T = 0 writes zero dweight and dbias.
+ * dx may equal x, dout or dres.  T = 0 writes zero dweight and dbias.  A row
+ * whose sum of squares passes the fp32 range counts as infinitely long (r = 0).
+ * Calls that share a workspace must be ordered on one stream.
  */
 moe_status_t moe_layer_norm_backward(int64_t num_tokens, int32_t hidden, moe_dtype_t dtype,
                                      float eps, const void* x, const void* weight,

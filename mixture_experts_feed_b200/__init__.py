@@ -592,6 +592,27 @@ def prepare_down_weights(w_down: torch.Tensor, stream=None) -> torch.Tensor:
 _ELEM = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
+def _expect_on(dev: int, t, name: str, shape, dtype, allow_none=False) -> None:
+    """``_expect`` for the tensors of a call after its first, which ``_expect``
+    has found on the current device ``dev`` (a small call's host time is
+    mostly such checks)."""
+    if t is not None and t.shape == shape and t.dtype == dtype and t.is_contiguous() \
+            and t.get_device() == dev:
+        return
+    _expect(t, name, shape, dtype, allow_none)
+
+
+def _ws_on(dev: int, ws) -> int:
+    if isinstance(ws, torch.Tensor) and ws.dtype == torch.uint8 and ws.is_contiguous() \
+            and ws.get_device() == dev:
+        return ws.data_ptr()
+    return _wsptr(ws)
+
+
+def _stream_on(dev: int, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 @dataclass(frozen=True)
 class GroupedMatmul:
     """Sizes of a matrix product grouped by expert: row operands of ``rows``
@@ -653,23 +674,25 @@ def new_norm_workspace(T: int, H: int, device=None) -> torch.Tensor:
 def moe_grouped_matmul(G: GroupedMatmul, a, w, expert_offsets, out, ws, stream=None):
     """``out[r] = a[r] @ w[e]^T`` for the rows r of each expert e."""
     _expect(a, "a", (G.rows, G.k), G.dtype)
-    _expect(w, "w", (G.E, G.n, G.k), G.dtype)
-    _expect(expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
-    _expect(out, "out", (G.rows, G.n), G.out)
+    dev = a.get_device()
+    _expect_on(dev, w, "w", (G.E, G.n, G.k), G.dtype)
+    _expect_on(dev, expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
+    _expect_on(dev, out, "out", (G.rows, G.n), G.out)
     _check(LIB.moe_grouped_matmul(ctypes.byref(G.desc()), _ptr(a), _ptr(w), _ptr(expert_offsets),
-                                  _ptr(out), _wsptr(ws), ws.numel(), _stream(stream)),
+                                  _ptr(out), _ws_on(dev, ws), ws.numel(), _stream_on(dev, stream)),
            "moe_grouped_matmul")
 
 
 def moe_grouped_matmul_dgrad(G: GroupedMatmul, dout, w, expert_offsets, da, ws, stream=None):
     """``da[r] = dout[r] @ w[e]``: the gradient of ``moe_grouped_matmul``'s rows."""
     _expect(dout, "dout", (G.rows, G.n), G.dtype)
-    _expect(w, "w", (G.E, G.n, G.k), G.dtype)
-    _expect(expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
-    _expect(da, "da", (G.rows, G.k), G.out)
+    dev = dout.get_device()
+    _expect_on(dev, w, "w", (G.E, G.n, G.k), G.dtype)
+    _expect_on(dev, expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
+    _expect_on(dev, da, "da", (G.rows, G.k), G.out)
     _check(LIB.moe_grouped_matmul_dgrad(ctypes.byref(G.desc()), _ptr(dout), _ptr(w),
-                                        _ptr(expert_offsets), _ptr(da), _wsptr(ws), ws.numel(),
-                                        _stream(stream)), "moe_grouped_matmul_dgrad")
+                                        _ptr(expert_offsets), _ptr(da), _ws_on(dev, ws), ws.numel(),
+                                        _stream_on(dev, stream)), "moe_grouped_matmul_dgrad")
 
 
 def moe_grouped_matmul_wgrad(G: GroupedMatmul, dout, a, expert_offsets, dw, ws, accumulate=False,
@@ -677,29 +700,36 @@ def moe_grouped_matmul_wgrad(G: GroupedMatmul, dout, a, expert_offsets, dw, ws, 
     """``dw[e] = dout_e^T @ a_e`` over each expert's rows (``accumulate``, fp32
     ``dw`` only: added to ``dw[e]``)."""
     _expect(dout, "dout", (G.rows, G.n), G.dtype)
-    _expect(a, "a", (G.rows, G.k), G.dtype)
-    _expect(expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
-    _expect(dw, "dw", (G.E, G.n, G.k), G.out)
+    dev = dout.get_device()
+    _expect_on(dev, a, "a", (G.rows, G.k), G.dtype)
+    _expect_on(dev, expert_offsets, "expert_offsets", (G.E + 1,), torch.int32)
+    _expect_on(dev, dw, "dw", (G.E, G.n, G.k), G.out)
     _check(LIB.moe_grouped_matmul_wgrad(ctypes.byref(G.desc()), _ptr(dout), _ptr(a),
                                         _ptr(expert_offsets), _ptr(dw), int(bool(accumulate)),
-                                        _wsptr(ws), ws.numel(), _stream(stream)),
+                                        _ws_on(dev, ws), ws.numel(), _stream_on(dev, stream)),
            "moe_grouped_matmul_wgrad")
 
 
-def _expect_swiglu(R: int, expert_offsets, perm_slot, topk_w) -> int:
+def _expect_slots(dev: int, t, name: str, R: int) -> None:
+    """A contiguous fp32 tensor of R entries, of any shape ([T, k] as well as [R])."""
+    if t.numel() != R:
+        raise ValueError(f"{name} must hold {R} entries, not {t.numel()}")
+    _expect_on(dev, t, name, t.shape, torch.float32)
+
+
+def _expect_swiglu(dev: int, R: int, expert_offsets, perm_slot, topk_w) -> int:
     """Checks of the arguments both SwiGLU entry points share; the number of groups."""
-    _expect(perm_slot, "perm_slot", (R,), torch.int32, allow_none=True)
-    if topk_w is None:
-        if perm_slot is not None:
-            raise ValueError("perm_slot needs topk_w")
-    else:
-        _expect(topk_w.reshape(-1) if topk_w.is_contiguous() else topk_w, "topk_w", (R,), torch.float32)
+    _expect_on(dev, perm_slot, "perm_slot", (R,), torch.int32, allow_none=True)
+    if topk_w is not None:
+        _expect_slots(dev, topk_w, "topk_w", R)
+    elif perm_slot is not None:
+        raise ValueError("perm_slot needs topk_w")
     if expert_offsets is None:
         return 0
     E = expert_offsets.numel() - 1
     if E < 1:
         raise ValueError("expert_offsets must hold E + 1 entries")
-    _expect(expert_offsets, "expert_offsets", (E + 1,), torch.int32)
+    _expect_on(dev, expert_offsets, "expert_offsets", (E + 1,), torch.int32)
     return E
 
 
@@ -713,13 +743,14 @@ def moe_swiglu_checkpoint(gu, expert_offsets, perm_slot, topk_w, h, q, scale, ws
     R, I = gu.shape[0], gu.shape[1] // 2
     code = _dtype_code(gu.dtype)
     _expect(gu, "gu", (R, 2 * I), gu.dtype)
-    E = _expect_swiglu(R, expert_offsets, perm_slot, topk_w)
-    _expect(h, "h", (R, I), gu.dtype)
-    _expect(q, "q", (R, 2 * I), torch.float8_e4m3fn)
-    _expect(scale, "scale", (R, I // 16), torch.uint8)
+    dev = gu.get_device()
+    E = _expect_swiglu(dev, R, expert_offsets, perm_slot, topk_w)
+    _expect_on(dev, h, "h", (R, I), gu.dtype)
+    _expect_on(dev, q, "q", (R, 2 * I), torch.float8_e4m3fn)
+    _expect_on(dev, scale, "scale", (R, I // 16), torch.uint8)
     _check(LIB.moe_swiglu_checkpoint(R, I, code, _ptr(gu), E, _ptr(expert_offsets), _ptr(perm_slot),
-                                     _ptr(topk_w), _ptr(h), _ptr(q), _ptr(scale), _wsptr(ws),
-                                     ws.numel(), _stream(stream)), "moe_swiglu_checkpoint")
+                                     _ptr(topk_w), _ptr(h), _ptr(q), _ptr(scale), _ws_on(dev, ws),
+                                     ws.numel(), _stream_on(dev, stream)), "moe_swiglu_checkpoint")
 
 
 def moe_swiglu_backward(q, scale, dh, expert_offsets, perm_slot, topk_w, dgu, d_topk_w, h, ws,
@@ -732,17 +763,17 @@ def moe_swiglu_backward(q, scale, dh, expert_offsets, perm_slot, topk_w, dgu, d_
     R, I = dh.shape
     code = _dtype_code(dh.dtype)
     _expect(dh, "dh", (R, I), dh.dtype)
-    _expect(q, "q", (R, 2 * I), torch.float8_e4m3fn)
-    _expect(scale, "scale", (R, I // 16), torch.uint8)
-    E = _expect_swiglu(R, expert_offsets, perm_slot, topk_w)
-    _expect(dgu, "dgu", (R, 2 * I), dh.dtype)
+    dev = dh.get_device()
+    _expect_on(dev, q, "q", (R, 2 * I), torch.float8_e4m3fn)
+    _expect_on(dev, scale, "scale", (R, I // 16), torch.uint8)
+    E = _expect_swiglu(dev, R, expert_offsets, perm_slot, topk_w)
+    _expect_on(dev, dgu, "dgu", (R, 2 * I), dh.dtype)
     if d_topk_w is not None:
-        _expect(d_topk_w.reshape(-1) if d_topk_w.is_contiguous() else d_topk_w, "d_topk_w", (R,),
-                torch.float32)
-    _expect(h, "h", (R, I), dh.dtype, allow_none=True)
+        _expect_slots(dev, d_topk_w, "d_topk_w", R)
+    _expect_on(dev, h, "h", (R, I), dh.dtype, allow_none=True)
     _check(LIB.moe_swiglu_backward(R, I, code, _ptr(q), _ptr(scale), _ptr(dh), E,
                                    _ptr(expert_offsets), _ptr(perm_slot), _ptr(topk_w), _ptr(dgu),
-                                   _ptr(d_topk_w), _ptr(h), _wsptr(ws), ws.numel(), _stream(stream)),
+                                   _ptr(d_topk_w), _ptr(h), _ws_on(dev, ws), ws.numel(), _stream_on(dev, stream)),
            "moe_swiglu_backward")
 
 
@@ -753,11 +784,12 @@ def moe_layer_norm(x, weight, bias, out, eps: float = 1e-6, stream=None):
     T, H = x.shape
     code = _dtype_code(x.dtype)
     _expect(x, "x", (T, H), x.dtype)
-    _expect(weight, "weight", (H,), x.dtype)
-    _expect(bias, "bias", (H,), x.dtype, allow_none=True)
-    _expect(out, "out", (T, H), x.dtype)
+    dev = x.get_device()
+    _expect_on(dev, weight, "weight", (H,), x.dtype)
+    _expect_on(dev, bias, "bias", (H,), x.dtype, allow_none=True)
+    _expect_on(dev, out, "out", (T, H), x.dtype)
     _check(LIB.moe_layer_norm(T, H, code, eps, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
-                              _stream(stream)), "moe_layer_norm")
+                              _stream_on(dev, stream)), "moe_layer_norm")
 
 
 def _expect_norm_backward(x, weight, dout, dx, dweight, dres):
@@ -766,12 +798,13 @@ def _expect_norm_backward(x, weight, dout, dx, dweight, dres):
     T, H = x.shape
     code = _dtype_code(x.dtype)
     _expect(x, "x", (T, H), x.dtype)
-    _expect(weight, "weight", (H,), x.dtype)
-    _expect(dout, "dout", (T, H), x.dtype)
-    _expect(dres, "dres", (T, H), x.dtype, allow_none=True)
-    _expect(dx, "dx", (T, H), x.dtype)
-    _expect(dweight, "dweight", (H,), torch.float32)
-    return T, H, code
+    dev = x.get_device()
+    _expect_on(dev, weight, "weight", (H,), x.dtype)
+    _expect_on(dev, dout, "dout", (T, H), x.dtype)
+    _expect_on(dev, dres, "dres", (T, H), x.dtype, allow_none=True)
+    _expect_on(dev, dx, "dx", (T, H), x.dtype)
+    _expect_on(dev, dweight, "dweight", (H,), torch.float32)
+    return dev, T, H, code
 
 
 def moe_layer_norm_backward(x, weight, dout, dx, dweight, dbias, ws, eps: float = 1e-6, dres=None,
@@ -779,19 +812,19 @@ def moe_layer_norm_backward(x, weight, dout, dx, dweight, dbias, ws, eps: float 
     """Gradients of ``moe_layer_norm``: ``dx`` (plus ``dres``, the residual
     path's gradient), ``dweight`` and ``dbias`` (may be None) in fp32; ``ws``
     from ``new_norm_workspace``."""
-    T, H, code = _expect_norm_backward(x, weight, dout, dx, dweight, dres)
-    _expect(dbias, "dbias", (H,), torch.float32, allow_none=True)
+    dev, T, H, code = _expect_norm_backward(x, weight, dout, dx, dweight, dres)
+    _expect_on(dev, dbias, "dbias", (H,), torch.float32, allow_none=True)
     _check(LIB.moe_layer_norm_backward(T, H, code, eps, _ptr(x), _ptr(weight), _ptr(dout),
-                                       _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias), _wsptr(ws),
-                                       ws.numel(), _stream(stream)), "moe_layer_norm_backward")
+                                       _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias), _ws_on(dev, ws),
+                                       ws.numel(), _stream_on(dev, stream)), "moe_layer_norm_backward")
 
 
 def moe_rmsnorm_backward(x, weight, dout, dx, dweight, ws, eps: float = 1e-6, dres=None, stream=None):
     """Gradients of ``moe_rmsnorm``, as ``moe_layer_norm_backward``."""
-    T, H, code = _expect_norm_backward(x, weight, dout, dx, dweight, dres)
+    dev, T, H, code = _expect_norm_backward(x, weight, dout, dx, dweight, dres)
     _check(LIB.moe_rmsnorm_backward(T, H, code, eps, _ptr(x), _ptr(weight), _ptr(dout), _ptr(dres),
-                                    _ptr(dx), _ptr(dweight), _wsptr(ws), ws.numel(),
-                                    _stream(stream)), "moe_rmsnorm_backward")
+                                    _ptr(dx), _ptr(dweight), _ws_on(dev, ws), ws.numel(),
+                                    _stream_on(dev, stream)), "moe_rmsnorm_backward")
 
 
 class InklingMoE:

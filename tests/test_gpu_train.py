@@ -148,6 +148,42 @@ def test_grouped_non_finite_values_stay_in_their_rows(form):
         th.check(o[rows], ref[rows], th.grouped_bound(ref, mag, m, BF)[rows], "other rows")
 
 
+def test_grouped_products_of_no_rows():
+    """A batch without rows: nothing is written but the weight gradient's zeros."""
+    for dtype, out in ((BF, BF), (BF, F32), (F32, F32)):
+        G = moe.GroupedMatmul(0, 3, 72, 40, dtype, out)
+        ws = moe.new_grouped_workspace(G)
+        z = lambda *s: torch.zeros(*s, dtype=dtype, device="cuda")   # noqa: E731
+        off = torch.zeros(4, dtype=torch.int32, device="cuda")
+        moe.moe_grouped_matmul(G, z(0, 40), z(3, 72, 40), off, z(0, 72).to(out), ws)
+        moe.moe_grouped_matmul_dgrad(G, z(0, 72), z(3, 72, 40), off, z(0, 40).to(out), ws)
+        dw = torch.full((3, 72, 40), 5.0, dtype=out, device="cuda")
+        moe.moe_grouped_matmul_wgrad(G, z(0, 72), z(0, 40), off, dw, ws)
+        assert bool((dw == 0).all())
+        if out == F32:
+            dw.fill_(5.0)
+            moe.moe_grouped_matmul_wgrad(G, z(0, 72), z(0, 40), off, dw, ws, accumulate=True)
+            assert bool((dw == 5.0).all())
+        assert moe.read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("form", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_grouped_infinite_and_nan_operands_stay_out_of_padding(form, dtype):
+    """The summed side ends inside a block of 64 and the outputs inside a tile:
+    what lies behind them in memory (here infinities in the next expert's
+    weights and rows) must not leak in."""
+    sizes, n, k = [33, 7], 72, 88
+    G, p, q, off, o = grouped_inputs(form, sizes, n, k, dtype, dtype)
+    p[33:] = float("inf")
+    q[(slice(33, None) if form == "wgrad" else 1)] = float("inf")
+    run_grouped(form, G, p, q, off, o)
+    mine = o[0] if form == "wgrad" else o[:33]
+    ref, mag, m = th.grouped_exact(form, p.nan_to_num(0, 0, 0), q.nan_to_num(0, 0, 0), off, torch.zeros_like(o))
+    pick = 0 if form == "wgrad" else slice(0, 33)
+    th.check(mine, ref[pick], th.grouped_bound(ref, mag, m, dtype)[pick], form)
+
+
 def test_grouped_bad_offsets_are_recorded():
     G, p, q, off, o = grouped_inputs("forward", [10, 10], 64, 64, BF, BF)
     ws = moe.new_grouped_workspace(G)
