@@ -14,9 +14,13 @@
 //   dg = w dh u s (1 + g (1 - s)),  du = w dh a,  dw = sum_j dh a u,
 // all in fp32, each output rounded once.
 //
-// Both passes are HBM-bound with little to spare for arithmetic.  A lane takes
-// 8 columns (4 pairs) at a time, so that every load and store of a warp is one
-// run of memory, and four of them are in flight before any is used.
+// Both passes are HBM-bound with little to spare for arithmetic (70 to 80
+// instructions a vector of 8 columns).  A lane takes 8 columns (4 pairs) at a
+// time, so that every load and store of a warp is one run of memory, and four
+// of them are in flight before any is used.  A team of lanes owns a row, so
+// that its weight is looked up once.  Measured on a B200 (65536 rows, I = 2048,
+// bf16): checkpoint 194 us (5.5 TB/s, 84% of the measured copy bandwidth; a
+// thread per 32 columns took 218 us), backward 224 us (6.0 TB/s, 91%; 310 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
