@@ -211,16 +211,206 @@ __global__ void __launch_bounds__(NT, TB == 64 ? 3 : 2) grouped_matmul_simt_kern
     for (int a = 0; a < M; ++a) {
       const int64_t i = i0 + ty * 4 + 64 * (a / 4) + a % 4;
       if (i >= ni) continue;
+      float v[M];
+#pragma unroll
+      for (int b = 0; b < M / 2; ++b) {
+        const float2 pr = unpack2(acc[a][b]);
+        v[2 * b] = pr.x, v[2 * b + 1] = pr.y;
+      }
+      if (FORM == kWgrad && g.accumulate) {          // a row's loads together, ahead of its stores
+#pragma unroll
+        for (int b = 0; b < M; ++b) {
+          const int64_t j = j0 + tx * 4 + 64 * (b / 4) + b % 4;
+          v[b] += j < cols ? elem_f32(out[i * cols + j]) : 0.0f;
+        }
+      }
 #pragma unroll
       for (int b = 0; b < M; ++b) {
         const int64_t j = j0 + tx * 4 + 64 * (b / 4) + b % 4;
-        if (j >= cols) continue;
-        O* dst = out + i * cols + j;
-        const float2 pr = unpack2(acc[a][b / 2]);
-        float v = b % 2 == 0 ? pr.x : pr.y;
-        if (FORM == kWgrad && g.accumulate) v += elem_f32(*dst);
-        *dst = elem_from<O>(v);
+        if (j < cols) out[i * cols + j] = elem_from<O>(v[b]);
       }
+    }
+  }
+}
+
+// Forward and dgrad of few rows, where tiles would be mostly padding and each
+// of their steps a wait for memory: W goes straight to registers, four to eight
+// loads of a thread in flight, against up to eight rows of P, which L1 serves.
+//   forward  a warp per two n: its lanes walk k, then add up
+//   dgrad    a block per 32 k: eight lanes of 4 k each for a row of W, 32 rows of
+//            W at a time, then the 32 partial sums add up
+// Each sum has one fixed order.  fp32, against the tiles (us):
+//   3 rows of 17 experts, n = 1024, k = 520     forward 10 / 35, dgrad 12 / 55
+//   64 of 1, n = k = 1024                       forward 35 / 57, dgrad 25 / 53
+//   64 of 1, n = k = 4096                       forward 222 / 209, dgrad 199 / 199
+//   512 of 64, n = k = 1024                     forward 207 / 258, dgrad 156 / 246
+//   256 of 16 (16 each), n = k = 1024           forward 98 / 80, dgrad 88 / 76
+// so it takes the calls of up to 64 rows, or of up to 8 rows an expert.  Bound by
+// the loads of P from L1 where rows are eight and by latency below that (512 of 64: 1.3
+// and 1.7 TB/s of weights).
+constexpr int kFewRows = 64;
+constexpr int kRowsAtOnce = 8;
+constexpr int kFewNs = 2;         // n of a warp of the forward product
+template <int R, typename T, typename O>
+__device__ __forceinline__ void few_rows_forward(const T* __restrict__ p, const T* __restrict__ w, int rows, int nr,
+                                                 int cols, int j0, int vec, O* __restrict__ out) {
+  constexpr int N = kFewNs, U = 2;                   // 4 loads of W in flight
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = j0 + N * warp;
+  if (j >= cols) return;                             // uniform over the warp
+  float acc[R][N];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int q = 0; q < N; ++q) acc[r][q] = 0.0f;
+  const T* wr[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) wr[q] = w + static_cast<int64_t>(min(j + q, cols - 1)) * nr;
+  if (vec) {                                         // nr is a multiple of 4: all four inside or none
+    for (int c0 = 4 * lane; c0 < nr; c0 += U * 128) {
+      float4 wv[U][N];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          wv[u][q] = c0 + u * 128 < nr ? load4(wr[q] + c0 + u * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rows)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (c0 + u * 128 >= nr) continue;
+            const float4 v = load4(p + static_cast<int64_t>(r) * nr + c0 + u * 128);
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+              acc[r][q] = fmaf(v.x, wv[u][q].x,
+                               fmaf(v.y, wv[u][q].y, fmaf(v.z, wv[u][q].z, fmaf(v.w, wv[u][q].w, acc[r][q]))));
+          }
+    }
+  } else {
+#pragma unroll 4
+    for (int c = lane; c < nr; c += 32) {
+      float wv[N];
+#pragma unroll
+      for (int q = 0; q < N; ++q) wv[q] = elem_f32(wr[q][c]);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < rows) {
+          const float v = elem_f32(p[static_cast<int64_t>(r) * nr + c]);
+#pragma unroll
+          for (int q = 0; q < N; ++q) acc[r][q] = fmaf(v, wv[q], acc[r][q]);
+        }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[r][q] += __shfl_xor_sync(0xffffffffu, acc[r][q], o);
+      if (lane == 0 && r < rows && j + q < cols) out[static_cast<int64_t>(r) * cols + j + q] = elem_from<O>(acc[r][q]);
+    }
+}
+
+constexpr int kFewCols = 32;      // columns of a dgrad tile
+template <int R, typename T, typename O>
+__device__ __forceinline__ void few_rows_dgrad(const T* __restrict__ p, const T* __restrict__ w, int rows, int nr,
+                                               int cols, int j0, int vec, float (*s_acc)[kRowsAtOnce][kFewCols],
+                                               O* __restrict__ out) {
+  constexpr int U = 8;                               // loads of W in flight
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane >> 3, jl = 4 * (lane & 7);
+  const int j = j0 + jl;
+  float acc[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[r][q] = 0.0f;
+  for (int c0 = 4 * warp + part; c0 < nr; c0 += U * (NT / 8)) {
+    float wv[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * (NT / 8);
+      const T* wr = w + static_cast<int64_t>(c) * cols + j;
+      if (vec) {                                     // cols is a multiple of 4: all four inside or none
+        const float4 v = c < nr && j < cols ? load4(wr) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        wv[u][0] = v.x, wv[u][1] = v.y, wv[u][2] = v.z, wv[u][3] = v.w;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) wv[u][q] = c < nr && j + q < cols ? elem_f32(wr[q]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < rows) {
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int c = c0 + u * (NT / 8);
+          d[u] = c < nr ? elem_f32(p[static_cast<int64_t>(r) * nr + c]) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[r][q] = fmaf(d[u], wv[u][q], acc[r][q]);
+      }
+  }
+  __syncthreads();                                   // the previous tile's sums are read
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      acc[r][q] += __shfl_xor_sync(0xffffffffu, acc[r][q], 8);
+      acc[r][q] += __shfl_xor_sync(0xffffffffu, acc[r][q], 16);
+    }
+    if (part == 0)
+      *reinterpret_cast<float4*>(&s_acc[warp][r][jl]) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+  }
+  __syncthreads();
+  const int r = threadIdx.x / kFewCols, c = threadIdx.x % kFewCols;   // NT = 8 rows of 32
+  if (r < rows && j0 + c < cols) {
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < NT / 32; ++q) v += s_acc[q][r][c];
+    out[static_cast<int64_t>(r) * cols + j0 + c] = elem_from<O>(v);
+  }
+}
+
+template <int FORM, typename T, typename O>
+__global__ void __launch_bounds__(NT) grouped_matmul_few_rows_kernel(const SimtProduct g) {
+  constexpr int R = kRowsAtOnce, COLS = FORM == kForward ? kFewNs * NT / 32 : kFewCols;   // columns of a tile
+  __shared__ __align__(16) float s_acc[FORM == kForward ? 1 : NT / 32][R][kFewCols];
+  __shared__ int s_bad;
+  extern __shared__ int s_tables[];
+  int* s_off = s_tables;
+  int* s_tile = s_tables + g.E + 1;
+  const int cols = FORM == kForward ? g.n : g.k, nr = FORM == kForward ? g.k : g.n;
+  if (threadIdx.x == 0) s_bad = 0;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  if (threadIdx.x < 32)
+    build_tile_prefix(g.offsets, g.E, 0, 0, kAllTiles, R, (cols + COLS - 1) / COLS, g.rows_cap, s_off, s_tile, &s_bad);
+  __syncthreads();
+  if (threadIdx.x == 0 && s_bad) record_status(g.status, DEV_BAD_ROW);
+  const int total = s_tile[g.E];
+  for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    int e, it, jt;
+    decode_tile(tile, s_tile, g.E, s_off, g.E, 0, kAllTiles, R, e, it, jt);
+    const int64_t row0 = static_cast<int64_t>(s_off[e]) + it * R;
+    const int rows = min(R, s_off[e + 1] - static_cast<int>(row0));
+    const T* p = static_cast<const T*>(g.p) + row0 * nr;
+    const T* w = static_cast<const T*>(g.q) + static_cast<int64_t>(e) * g.n * g.k;
+    O* out = static_cast<O*>(g.out) + row0 * cols;
+    if (FORM == kForward) {
+      if (rows <= 2)
+        few_rows_forward<2>(p, w, rows, nr, cols, jt * COLS, g.vec_q, out);
+      else
+        few_rows_forward<R>(p, w, rows, nr, cols, jt * COLS, g.vec_q, out);
+    } else {
+      if (rows <= 2)
+        few_rows_dgrad<2>(p, w, rows, nr, cols, jt * COLS, g.vec_q, s_acc, out);
+      else
+        few_rows_dgrad<R>(p, w, rows, nr, cols, jt * COLS, g.vec_q, s_acc, out);
     }
   }
 }
@@ -244,7 +434,22 @@ cudaError_t launch_tile(const GroupedProduct& g, int num_sms, cudaStream_t strea
 }
 
 template <int FORM, typename T, typename O>
+cudaError_t launch_few_rows(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
+  SimtProduct s{g.p, g.q, g.out, g.offsets, g.status, g.E, g.n, g.k, static_cast<int>(g.rows), 0, 0, 0};
+  s.vec_q = g.k % 4 == 0;
+  const size_t smem = sizeof(int) * (2 * static_cast<size_t>(g.E) + 2);
+  const int64_t tiles = std::min<int64_t>(g.rows, ceil_div(g.rows, kRowsAtOnce) + g.E) *
+                        (FORM == kForward ? ceil_div(g.n, kFewNs * NT / 32) : ceil_div(g.k, kFewCols));
+  const unsigned grid = static_cast<unsigned>(
+      std::max<int64_t>(1, std::min<int64_t>(tiles, static_cast<int64_t>(num_sms) * 8)));
+  return launch_chained(grouped_matmul_few_rows_kernel<FORM, T, O>, grid, NT, smem, stream, s);
+}
+
+template <int FORM, typename T, typename O>
 cudaError_t launch_form(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
+  if constexpr (FORM != kWgrad)
+    if (g.rows <= kFewRows || g.rows <= kRowsAtOnce * static_cast<int64_t>(g.E))
+      return launch_few_rows<FORM, T, O>(g, num_sms, stream);
   // rows / 128 + E bounds the tiles from above by E: full tiles alone count
   const int64_t full = FORM == kWgrad ? tile_bound<FORM>(g, 128)
                                       : g.rows / 128 * ceil_div(FORM == kForward ? g.n : g.k, 128);

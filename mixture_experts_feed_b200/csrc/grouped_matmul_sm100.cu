@@ -66,6 +66,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "grouping.cuh"
 #include "internal.h"
 #include "sm100_ptx.cuh"
 
@@ -125,32 +126,11 @@ __device__ __forceinline__ int even_height(int n) {
   return (tiles_over(n, t > 0 ? t : 1) + 31) & ~31;
 }
 
-// Warp: s_off = the offsets (clamped to an ascending sequence inside
-// [0, cap] when they are not one), s_tile = exclusive prefix of tile counts.
+// Warp: s_off = the checked offsets, s_tile = exclusive prefix of tile counts.
 template <int FORM>
 __device__ __forceinline__ void build_tables(const ProductParams& p, int* s_off, int* s_tile, int* bad) {
   const int lane = threadIdx.x & 31;
-  bool wrong = false;
-  for (int i = lane; i <= p.E; i += 32) {
-    const int v = p.offsets[i];
-    const int next = i < p.E ? p.offsets[i + 1] : p.rows_cap;
-    wrong |= v < 0 || v > next || v > p.rows_cap || (i == 0 && v != 0);
-    s_off[i] = v;
-  }
-  __syncwarp();
-  if (__any_sync(0xffffffffu, wrong)) {
-    if (lane == 0) {
-      *bad = 1;
-      int prev = 0;
-      for (int i = 0; i <= p.E; ++i) {
-        int v = i == 0 ? 0 : s_off[i];
-        v = v < prev ? prev : (v > p.rows_cap ? p.rows_cap : v);
-        s_off[i] = v;
-        prev = v;
-      }
-    }
-    __syncwarp();
-  }
+  load_offsets(p.offsets, p.E, p.rows_cap, s_off, bad);
   const int ct = tiles_over(p.n_j, TM);
   int carry = 0;
   if (lane == 0) s_tile[0] = 0;

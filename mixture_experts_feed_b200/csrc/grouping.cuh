@@ -92,35 +92,48 @@ __device__ __forceinline__ int tile_first_row(int m, int rows, int set, int bm) 
   return set == kPairs ? m * 2 * bm : m * bm;
 }
 
-// Warp 0 of the block fills s_off[0..E] from global memory and
+// A warp fills s_off[0..E] from global memory.  Offsets outside [0, rows_cap]
+// or decreasing are clamped to an empty group and reported through `bad` (set
+// to 1); one lane walks the offsets for that only when a check by all lanes
+// finds such a one.
+__device__ inline void load_offsets(const int32_t* __restrict__ offsets, int E, int rows_cap, int* s_off,
+                                    int* bad) {
+  const int lane = threadIdx.x & 31;
+  bool wrong = false;
+  for (int i = lane; i <= E; i += 32) {
+    const int v = offsets[i];
+    const int next = i < E ? offsets[i + 1] : rows_cap;
+    wrong |= v < 0 || v > next || v > rows_cap || (i == 0 && v != 0);
+    s_off[i] = v;
+  }
+  __syncwarp();
+  if (__any_sync(0xffffffffu, wrong)) {
+    if (lane == 0) {
+      *bad = 1;
+      int prev = 0;
+      for (int i = 0; i <= E; ++i) {
+        int v = i == 0 ? 0 : s_off[i];
+        v = v < prev ? prev : (v > rows_cap ? rows_cap : v);
+        s_off[i] = v;
+        prev = v;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Warp 0 of the block fills s_off[0..E] from global memory (load_offsets) and
 // s_tile[0..G] with the exclusive prefix of per-group tile counts.
-// Offsets outside [0, rows_cap] or decreasing are clamped to an empty group
-// and reported through `bad` (set to 1).
 __device__ inline void build_tile_prefix(const int32_t* __restrict__ offsets, int E, int S,
                                          int64_t T, int set, int bm, int n_tiles, int rows_cap,
                                          int* s_off, int* s_tile, int* bad) {
   const int lane = threadIdx.x & 31;
   if (E == 0) {
     if (lane == 0) s_off[0] = 0;
+    __syncwarp();
   } else {
-    for (int i = lane; i <= E; i += 32) s_off[i] = offsets[i];
+    load_offsets(offsets, E, rows_cap, s_off, bad);
   }
-  __syncwarp();
-  if (lane == 0 && E > 0) {
-    // clamp to a monotone sequence inside [0, rows_cap]
-    int prev = 0;
-    for (int i = 0; i <= E; ++i) {
-      int v = s_off[i];
-      if (v < prev || v > rows_cap || (i == 0 && v != 0)) {
-        *bad = 1;
-        v = v < prev ? prev : (v > rows_cap ? rows_cap : v);
-        if (i == 0) v = 0;
-      }
-      s_off[i] = v;
-      prev = v;
-    }
-  }
-  __syncwarp();
   const int G = E + S;
   int carry = 0;
   if (lane == 0) s_tile[0] = 0;

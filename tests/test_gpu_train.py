@@ -89,6 +89,14 @@ def test_grouped_group_sizes(form, sizes):
     check_grouped(form, sizes, 264, 328, BF, BF, pad=5)
 
 
+@pytest.mark.parametrize("form", ["forward", "dgrad"])
+@pytest.mark.parametrize("sizes", [[1], [3, 0, 9, 8, 0, 1], [64], [0, 50], [63]])
+@pytest.mark.parametrize("n,k", [(64, 128), (33, 51), (200, 4), (7, 260)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_grouped_few_rows_on_the_cuda_cores(form, sizes, n, k, dtype):
+    check_grouped(form, sizes, n, k + (dtype == BF), dtype, dtype, pad=64 - sum(sizes))
+
+
 @pytest.mark.parametrize("sizes", [RAGGED, [0, 0], [3000, 0, 1]])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_wgrad_accumulates(sizes, dtype):
