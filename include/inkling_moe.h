@@ -485,8 +485,11 @@ typedef struct {
   int32_t out_dtype;  /* moe_elem_t of the output: dtype, or MOE_ELEM_F32 */
 } moe_grouped_desc_t;
 
-/* Workspace bytes of the three products below.  Its head is the status word:
- * initialise it once with moe_workspace_init(). */
+/* Workspace bytes of the three products below (out_dtype does not matter).
+ * Its head is the status word: initialise it once with moe_workspace_init().
+ * 256 bytes, and up to 39 MB more for the sizes whose products may be cut
+ * along the sum (few output tiles and a long sum; see below): partial sums,
+ * with nothing in them to initialise or to keep. */
 moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* bytes);
 
 /*
@@ -505,9 +508,12 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* 
  * Offsets that decrease or leave [0, R] are recorded in the status word
  * (MOE_ERR_DEVICE_CHECK) and read as the nearest valid ones.
  * bf16 and fp16 operands with n % 8 == 0 and k % 8 == 0 run on the tensor
- * cores (one launch for all experts); fp32 operands and other sizes on the
- * CUDA cores.  An fp16 output past 65504 becomes an infinity.  Outputs must
- * not overlap operands.  R = 0: the first two launch nothing; the third still
+ * cores, all experts in one launch.  Where its tiles could leave half of the
+ * SMs idle (few columns, few rows or few experts) and the sum is long (more
+ * than 47 x 64 terms), tiles may be cut along the sum and a second launch adds
+ * the parts, in a fixed order.  fp32 operands and other sizes run on the CUDA
+ * cores.  An fp16 output past 65504 becomes an infinity.  Outputs must not
+ * overlap operands.  R = 0: the first two launch nothing; the third still
  * reads expert_offsets and writes dW.
  */
 moe_status_t moe_grouped_matmul(const moe_grouped_desc_t* desc, const void* a, const void* w,

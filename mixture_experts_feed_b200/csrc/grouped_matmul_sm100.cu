@@ -39,6 +39,16 @@
 // largest input gradient, 512 nothing.  16-bit outputs round away hundreds of
 // times more and take one chain.
 //
+// Few tiles with a long sum (the weight gradient of one large expert, a
+// product of few rows with a long k) would leave most pairs idle.  Such tiles are cut
+// along r into pieces, each a tile of its own whose accumulator goes to a slot
+// of the workspace, and a second kernel adds a tile's slots in order:
+// reproducible, where adds to memory would not be.  Measured (us, cut / whole):
+// dW of one expert of 16384 rows, 256 x 256, 24 / 84; of 8192 rows, 1024 x 1024,
+// 34 / 50; 65536 rows all in one of 64 experts, 512 x 512, 59 / 305; 249 rows,
+// k = 4096, n = 1024, 23 / 29.  Now 12 us of launches and drain, the loads, and the
+// slots through L2.
+//
 // Roles (one CTA an SM): warp 0 loads, warp 1 allocates tensor memory and
 // (rank 0) issues the MMAs, warp 10 works the tiles out, warp 11 mends wgrad's
 // partial blocks, warps 2..9 store (through staging boxes and TMA stores;
@@ -59,6 +69,7 @@
 // TB/s; 24576 rows of 64 experts, n = k = 2048: forward 930, dW 885 TFLOP/s
 // at 3.2 TB/s.  DRAM traffic is the algorithm's (forward: 638 MB read for 637,
 // dW 201 for 201).  Six decoded rows (50 MB of weights) take 15 us.
+#include <algorithm>
 #include <atomic>
 
 #include <cuda.h>
@@ -91,18 +102,32 @@ constexpr int TQ = 8;                    // slots of the tile queue
 constexpr int kBand = 8;                 // i tiles per band (tile order)
 constexpr int kChain = 8;                // blocks of 64 per accumulation chain, fp32 outputs
 constexpr int kMaxSmem = 232448;         // shared memory a block can have
+constexpr int kSplitUnits = 74;          // CTA pairs that pieces are made for
+constexpr int kMinPiece = 8;             // blocks of 64 r of a piece, at least
+constexpr int kMinGain = 24;             // blocks that cutting saves the longest tile, at least
+constexpr int64_t kSkewedRows = 16384;   // wgrad: rows from which skewed groups are provided for
+constexpr int kCutWord = 32;             // word of the status region behind the status and the counters
+constexpr int kJoinRows = 4;             // i of a step of the joining kernel
 
-struct alignas(64) ProductParams {
+// What the tables are made of.
+struct Shape {
+  const int32_t* offsets;
+  int E, rows_cap;
+  int n_i, n_j, n_r;     // sizes of i, j, r (0 where it is the group's rows)
+  int accumulate;
+  int units;             // split products: CTA pairs of the launch
+  int slot_i, slot_j;    // split products: a piece's slot [slot_i][slot_j] of fp32
+  int32_t* cut;          // split products: where the first kernel says how many slots it filled
+};
+
+struct alignas(64) ProductParams : Shape {
   CUtensorMap tmM;       // M side
   CUtensorMap tmN[4];    // N side: boxes of 128, 64, 32 and 16 rows (wgrad: [0] alone)
   CUtensorMap tmOut;     // output [depth][i][j]: boxes of 64 j x 64 i (16-bit) or 32 x 32 (fp32)
   CUtensorMap tmOut32;   // 16-bit: boxes of 64 j x 32 i
-  const int32_t* offsets;
+  CUtensorMap tmParts;   // split products: the slots [slots x slot_i][slot_j], boxes of 32 x 32
   int32_t* status;
   void* out;
-  int E, rows_cap;
-  int n_i, n_j, n_r;     // sizes of i, j, r (0 where it is the group's rows)
-  int accumulate;
   uint32_t fmt;          // operand format bits of the MMA descriptor
   int stages;            // pipeline stages
 };
@@ -111,24 +136,24 @@ struct Smem {
   // full[STAGES], empty[STAGES], tail[STAGES], tfull[2], tempty[2], drain, tq[TQ], tqe[TQ], pair[4]
   static constexpr int kNumBars = 3 * STAGES + 9 + 2 * TQ;
   // the stages, 4 KB of staging a warp, the tile queue, the barriers, then
-  // tmem base, abort, bad, then s_off[E + 1], s_tile[E + 1]
+  // tmem base, abort, bad, piece, then s_off[E + 1], s_tile[E + 1] (split: s_slot[E + 1])
   static constexpr int kFixed = TQ * 32 + kNumBars * 8 + 16;
-  static int bytes(int E, int stages) {
-    return 1024 + stages * STAGE_BYTES + EPI_WARPS * OUT_BYTES + kFixed + 8 * (E + 1);
+  static int bytes(int E, int stages, bool split) {
+    return 1024 + stages * STAGE_BYTES + EPI_WARPS * OUT_BYTES + kFixed + (split ? 12 : 8) * (E + 1);
   }
 };
 
 __host__ __device__ __forceinline__ int tiles_over(int n, int t) { return (n + t - 1) / t; }
 
 // Height of a side of `n` cut into tiles of at most TN: even, a multiple of 32.
-__device__ __forceinline__ int even_height(int n) {
+__host__ __device__ __forceinline__ int even_height(int n) {
   const int t = tiles_over(n, TN);
   return (tiles_over(n, t > 0 ? t : 1) + 31) & ~31;
 }
 
 // Warp: s_off = the checked offsets, s_tile = exclusive prefix of tile counts.
 template <int FORM>
-__device__ __forceinline__ void build_tables(const ProductParams& p, int* s_off, int* s_tile, int* bad) {
+__device__ __forceinline__ void build_tables(const Shape& p, int* s_off, int* s_tile, int* bad) {
   const int lane = threadIdx.x & 31;
   load_offsets(p.offsets, p.E, p.rows_cap, s_off, bad);
   const int ct = tiles_over(p.n_j, TM);
@@ -154,36 +179,94 @@ __device__ __forceinline__ void build_tables(const ProductParams& p, int* s_off,
   __syncwarp();
 }
 
-struct alignas(32) TileInfo {
-  int e;         // group
-  int row0;      // the group's first row
-  int rows;      // its rows
-  int i0, j0;    // tile origin (i inside the group for forward and dgrad)
-  int ni;        // valid i in the tile
-  int mma_n;     // N of its MMAs: ni rounded up to 32
-  int blocks;    // blocks of 64 r; -1: no more tiles
-};
+// Warp: the tables of a split product.  A tile of group e sums over
+// group_blocks(e) blocks of r; in ceil(blocks / *s_piece) pieces of even
+// length.  Pieces are as long as every pair's share of all blocks, at least
+// kMinPiece, and a little longer where the pieces would otherwise make a
+// second round; nothing is cut for less than kMinGain blocks.  s_tile = exclusive prefix of the pieces (JOIN: of the tiles of
+// more than one piece), s_slot = exclusive prefix of the pieces of such tiles: fewer than
+// 2 x units, because every tile in pieces has more blocks than a pair's share.
+template <int FORM> __device__ __forceinline__ int group_tiles(const Shape& p, const int* s_off, int e) {
+  return tiles_over(FORM == kWgrad ? p.n_i : s_off[e + 1] - s_off[e], TN) * tiles_over(p.n_j, TM);
+}
+template <int FORM> __device__ __forceinline__ int group_blocks(const Shape& p, const int* s_off, int e) {
+  return tiles_over(FORM == kWgrad ? s_off[e + 1] - s_off[e] : p.n_r, BK);
+}
+template <int FORM, bool JOIN>
+__device__ __forceinline__ void build_split_tables(const Shape& p, int* s_off, int* s_tile, int* s_slot,
+                                                   int* s_piece, int* bad) {
+  const int lane = threadIdx.x & 31;
+  load_offsets(p.offsets, p.E, p.rows_cap, s_off, bad);
+  int64_t work = 0;
+  int live = 0, longest = 0;                               // tiles with blocks, the most blocks of one
+  for (int e = lane; e < p.E; e += 32) {
+    const int t = group_tiles<FORM>(p, s_off, e), b = group_blocks<FORM>(p, s_off, e);
+    work += static_cast<int64_t>(t) * b;
+    live += b > 0 ? t : 0;
+    longest = max(longest, t > 0 ? b : 0);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    work += __shfl_xor_sync(0xffffffffu, work, d);
+    live += __shfl_xor_sync(0xffffffffu, live, d);
+  }
+  int piece = max(kMinPiece, static_cast<int>((work + p.units - 1) / p.units));
+  for (int round = 0; round < 8 && live <= p.units; ++round) {
+    int pieces = 0;
+    for (int e = lane; e < p.E; e += 32)
+      pieces += group_tiles<FORM>(p, s_off, e) * tiles_over(group_blocks<FORM>(p, s_off, e), piece);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, d);
+    if (pieces <= p.units) break;
+    piece += max(1, piece >> 3);
+  }
+  if (longest - piece < kMinGain) piece = max(piece, longest);
+  int carry = 0, slots = 0;
+  if (lane == 0) {
+    *s_piece = piece;
+    s_tile[0] = 0;
+    s_slot[0] = 0;
+  }
+  for (int base = 0; base < p.E; base += 32) {
+    const int e = base + lane;
+    int cnt = 0, cut = 0;
+    if (e < p.E) {
+      const int t = group_tiles<FORM>(p, s_off, e), b = group_blocks<FORM>(p, s_off, e);
+      const int pieces = tiles_over(b, piece);
+      cut = pieces > 1 ? t * pieces : 0;
+      cnt = JOIN ? (pieces > 1 ? t : 0) : FORM == kWgrad && p.accumulate && b == 0 ? 0 : t * max(pieces, 1);
+    }
+    int incl = cnt, incl_cut = cut;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d), w = __shfl_up_sync(0xffffffffu, incl_cut, d);
+      if (lane >= d) { incl += v; incl_cut += w; }
+    }
+    if (e < p.E) {
+      s_tile[e + 1] = carry + incl;
+      s_slot[e + 1] = slots + incl_cut;
+    }
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+    slots += __shfl_sync(0xffffffffu, incl_cut, 31);
+  }
+  __syncwarp();
+}
 
-// Tile `tile` of the launch.  Inside a group the shorter tile side runs
-// innermost (consecutive tiles share the other side's operand from L2); when
-// both are long, bands of kBand i tiles, j by j inside a band.
-template <int FORM>
-__device__ __forceinline__ TileInfo tile_info(int tile, const ProductParams& p, const int* s_off,
-                                              const int* s_tile) {
-  int lo = 0, hi = p.E - 1;
+// Group whose run of the prefix table holds `tile`.
+__device__ __forceinline__ int find_group(int tile, int E, const int* s_tile) {
+  int lo = 0, hi = E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (s_tile[mid] <= tile) lo = mid; else hi = mid - 1;
   }
-  TileInfo t;
-  t.e = lo;
-  t.row0 = s_off[lo];
-  t.rows = s_off[lo + 1] - s_off[lo];
-  const int n_i = FORM == kWgrad ? p.n_i : t.rows;
-  const int n_r = FORM == kWgrad ? t.rows : p.n_r;
-  const int it = tiles_over(n_i, TN), jt = tiles_over(p.n_j, TM);
-  const int local = tile - s_tile[lo];
-  int i, j;
+  return lo;
+}
+
+// Tile `local` of a group of it x jt tiles.  The shorter tile side runs
+// innermost (consecutive tiles share the other side's operand from L2); when
+// both are long, bands of kBand i tiles, j by j inside a band.
+__device__ __forceinline__ void tile_at(int local, int it, int jt, int& i, int& j) {
   if (it > kBand && jt > kBand) {
     const int band = local / (kBand * jt);
     const int in_band = local - band * kBand * jt;
@@ -197,12 +280,66 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const ProductParams& p, 
     j = local / it;
     i = local - j * it;
   }
+}
+
+struct alignas(32) TileInfo {
+  int e;         // group
+  int row0;      // the group's first row
+  int rows;      // its rows
+  int i0, j0;    // tile origin (i inside the group for forward and dgrad)
+  int ni;        // valid i in the tile
+  int mma_n;     // N of its MMAs: ni rounded up to 32
+  int blocks;    // blocks of 64 r; -1: no more tiles
+};
+
+// Piece `tile` of a split product: the tile's blocks are the piece's, so a piece
+// of a weight gradient is a tile of fewer rows; forward and dgrad, which do not
+// use `rows`, have the piece's first block there.  Bits 10 and up of e:
+// 1 + the piece's slot, or 0 for a tile in one piece.
+constexpr int kGroupBits = 10;
+template <bool SPLIT> __device__ __forceinline__ int group_of(const TileInfo& t) {
+  return SPLIT ? t.e & ((1 << kGroupBits) - 1) : t.e;
+}
+
+// Tile `tile` of the launch.
+template <int FORM, bool SPLIT>
+__device__ __forceinline__ TileInfo tile_info(int tile, const Shape& p, const int* s_off, const int* s_tile,
+                                              const int* s_slot, int piece) {
+  TileInfo t;
+  const int e = find_group(tile, p.E, s_tile);
+  t.e = e;
+  t.row0 = s_off[e];
+  t.rows = s_off[e + 1] - s_off[e];
+  const int n_i = FORM == kWgrad ? p.n_i : t.rows;
+  const int n_r = FORM == kWgrad ? t.rows : p.n_r;
+  const int it = tiles_over(n_i, TN), jt = tiles_over(p.n_j, TM);
+  int local = tile - s_tile[e];
+  t.blocks = tiles_over(n_r, BK);
+  if (SPLIT) {
+    const int pieces = tiles_over(t.blocks, piece);
+    int first = 0;
+    if (pieces > 1) {
+      t.e |= (1 + s_slot[e] + local) << kGroupBits;
+      const int mine = local / (it * jt);
+      local -= mine * it * jt;
+      const int each = tiles_over(t.blocks, pieces);      // mine * each < blocks for every piece
+      first = mine * each;
+      t.blocks = min(each, t.blocks - first);
+    }
+    if (FORM == kWgrad) {
+      t.row0 += first * BK;
+      t.rows = min(t.rows - first * BK, t.blocks * BK);
+    } else {
+      t.rows = first;
+    }
+  }
+  int i, j;
+  tile_at(local, it, jt, i, j);
   const int h = even_height(n_i);
   t.i0 = i * h;
   t.j0 = j * TM;
   t.ni = min(h, n_i - t.i0);
   t.mma_n = (t.ni + 31) & ~31;
-  t.blocks = tiles_over(n_r, BK);
   return t;
 }
 
@@ -317,12 +454,27 @@ __device__ __forceinline__ void flush(const ProductParams& p, const OutStage& os
   __syncwarp();
 }
 
+template <int OUT> struct Elem {
+  using type = float;
+  static __device__ __forceinline__ float from(float v) { return v; }
+};
+template <> struct Elem<MOE_ELEM_BF16> {
+  using type = __nv_bfloat16;
+  static __device__ __forceinline__ __nv_bfloat16 from(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Elem<MOE_ELEM_F16> {
+  using type = __half;
+  static __device__ __forceinline__ __half from(float v) { return __float2half_rn(v); }
+};
+
 template <int FORM> struct Majors {
   static constexpr bool M_MN = FORM != kForward;   // M side MN-major (j contiguous)
   static constexpr bool N_MN = FORM == kWgrad;     // N side MN-major (i contiguous)
 };
 
-template <int FORM, int OUT>
+// SPLIT: tiles in pieces along r (build_split_tables), which are stored to their
+// slots as fp32; whole tiles go to the output as without it.
+template <int FORM, int OUT, bool SPLIT>
 __global__ void __launch_bounds__(num_threads(FORM), 1)
     grouped_matmul_kernel(const __grid_constant__ ProductParams p) {
   constexpr bool M_MN = Majors<FORM>::M_MN, N_MN = Majors<FORM>::N_MN;
@@ -349,6 +501,8 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
   // blocks of 64 r that one accumulation chain takes
   constexpr int kRun = F32 ? kChain : (1 << 30);
   int* s_tile = s_off + (p.E + 1);
+  int* s_slot = s_tile + (p.E + 1);      // split products
+  int* s_piece = s_bad + 1;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // warp-uniform
   const int lane = threadIdx.x & 31;
@@ -391,7 +545,14 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
   }
   __syncthreads();                       // *s_bad = 0 before warp 2 may set it
   pdl_wait();
-  if (warp == 2) build_tables<FORM>(p, s_off, s_tile, s_bad);
+  if (warp == 2) {
+    if (SPLIT) {
+      build_split_tables<FORM, false>(p, s_off, s_tile, s_slot, s_piece, s_bad);
+      if (blockIdx.x == 0 && lane == 0) *p.cut = s_slot[p.E];
+    } else {
+      build_tables<FORM>(p, s_off, s_tile, s_bad);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();                        // both CTAs' barriers exist before any cross-CTA signal
@@ -442,7 +603,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         if (!all_wait(&empty[stage], phase ^ 1u, s_abort, p.status)) { ok = false; break; }
         uint8_t* m_dst = smem + stage * STAGE_BYTES;
         uint8_t* n_dst = m_dst + SIDE_BYTES;
-        const int r = b * BK;
+        const int r = (SPLIT && FORM != kWgrad ? t.rows + b : b) * BK;
         // wgrad: a last block past the group's rows completes on this CTA's own barrier
         const bool partial = FORM == kWgrad && r + BK > t.rows;
         if (elect_one()) {
@@ -458,10 +619,10 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
             bar = mapa_shared(&full[stage], 0);
           }
           if (!M_MN) {
-            tma_load_3d_pair(m_dst, &p.tmM, bar, r, j, t.e);
+            tma_load_3d_pair(m_dst, &p.tmM, bar, r, j, group_of<SPLIT>(t));
           } else if (FORM == kDgrad) {
-            tma_load_3d_pair(m_dst, &p.tmM, bar, j, r, t.e);
-            tma_load_3d_pair(m_dst + 8192, &p.tmM, bar, j + 64, r, t.e);
+            tma_load_3d_pair(m_dst, &p.tmM, bar, j, r, group_of<SPLIT>(t));
+            tma_load_3d_pair(m_dst + 8192, &p.tmM, bar, j + 64, r, group_of<SPLIT>(t));
           } else {
             tma_load_2d_pair(m_dst, &p.tmM, bar, j, t.row0 + r);
             tma_load_2d_pair(m_dst + 8192, &p.tmM, bar, j + 64, t.row0 + r);
@@ -574,7 +735,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
       const int64_t tile = unit + static_cast<int64_t>(seq) * units;
       TileInfo t;
       t.blocks = -1;
-      if (tile < total) t = tile_info<FORM>(static_cast<int>(tile), p, s_off, s_tile);
+      if (tile < total) t = tile_info<FORM, SPLIT>(static_cast<int>(tile), p, s_off, s_tile, s_slot, *s_piece);
       if (!all_wait(&tqe[slot], ((seq / TQ) & 1) ^ 1u, s_abort, p.status)) break;
       if (elect_one()) {
         s_tq[slot] = t;
@@ -632,7 +793,8 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
     for (int seq = 0; ok && take(seq, t); ++seq) {
       const int j = t.j0 + rank * 128 + quarter * 32;
       const int row = FORM == kWgrad ? t.i0 : t.row0 + t.i0;   // output row of column 0
-      const int depth = FORM == kWgrad ? t.e : 0;
+      const int depth = FORM == kWgrad ? group_of<SPLIT>(t) : 0;
+      const int slot = SPLIT ? (t.e >> kGroupBits) - 1 : -1;
       if (F32) {
         // the tile's chains added in registers, in order
         float sum[4][32];
@@ -673,7 +835,15 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
               for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(os.buf + i * 128 + lane * 4) = sum[x][i];
               fence_proxy_async_smem();
               __syncwarp();
-              flush<FORM, 4>(p, os, j, row + c, depth, t.ni - c, lane);
+              if (SPLIT && slot >= 0) {                    // a whole box: the slot is this piece's alone
+                if (elect_one()) {
+                  tma_store_3d(&p.tmParts, os.buf, j - t.j0, slot * p.slot_i + c, 0);
+                  bulk_commit_group();
+                }
+                __syncwarp();
+              } else {
+                flush<FORM, 4>(p, os, j, row + c, depth, t.ni - c, lane);
+              }
             }
           }
         }
@@ -688,6 +858,33 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty[acc], 0));
         };
+        if (SPLIT && slot >= 0) {
+          // a piece: fp32 boxes of its warp's own, each warp in its half of the
+          // two warps' buffer, which the issuer's last store may still be reading
+          if (elect_one()) bulk_wait_group_read0();
+          if (!os.pair_sync()) { ok = false; break; }
+          uint8_t* buf = os.buf + (quarter & 1) * OUT_BYTES;
+#pragma unroll 1
+          for (int c = part * 32; c < t.ni && j < p.n_j; c += 64) {
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
+            tmem_ld_wait();
+            if (elect_one()) bulk_wait_group_read0();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) *reinterpret_cast<uint32_t*>(buf + i * 128 + lane * 4) = v[i];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (elect_one()) {
+              tma_store_3d(&p.tmParts, buf, j - t.j0, slot * p.slot_i + c, 0);
+              bulk_commit_group();
+            }
+            __syncwarp();
+          }
+          release();
+          ++it;
+          continue;
+        }
 #pragma unroll 1
         for (int c = part * 64; c < t.ni; c += 128) {
           uint32_t v[64];                                  // [lane half][column half][16]
@@ -718,7 +915,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
                 w[i] = pack_bf16x2(lo, hi);
               }
             }
-            if (os.issuer && elect_one()) bulk_wait_group_read0();
+            if ((SPLIT || os.issuer) && elect_one()) bulk_wait_group_read0();   // split: a piece's boxes too
             if (!os.pair_sync()) { ok = false; break; }
             // w[16 h16 + 8 half + 2 n + h8]: j 16 h16 + 8 h8 .., i 32 half + 8 n ..
 #pragma unroll
@@ -747,6 +944,99 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, TMEM_COLS);
+  }
+}
+
+// The pieces of a split product's tiles, added in order and rounded once.  A
+// step is 256 j by kJoinRows i, or by four times as many where there are steps
+// enough for every block: a thread takes four j, of V i, with 16 loads in flight.
+struct JoinParams : Shape {
+  const float* parts;
+  void* out;
+};
+
+template <int FORM, int OUT, int V>
+__device__ __forceinline__ void join_step(const JoinParams& p, int step, int steps, const int* s_off,
+                                          const int* s_tile, const int* s_slot) {
+  using O = typename Elem<OUT>::type;
+  constexpr int U = 16 / V;
+  const int tile = step / steps, i0 = (step - tile * steps) * (kJoinRows * V) + (threadIdx.x >> 6);
+  const int e = find_group(tile, p.E, s_tile);
+  const int n_i = FORM == kWgrad ? p.n_i : s_off[e + 1] - s_off[e];
+  const int it = tiles_over(n_i, TN), jt = tiles_over(p.n_j, TM);
+  const int local = tile - s_tile[e];
+  int i, j;
+  tile_at(local, it, jt, i, j);
+  const int h = even_height(n_i), jj = (threadIdx.x & 63) * 4;
+  const int ni = min(h, n_i - i * h);
+  if (i0 >= ni || j * TM + jj >= p.n_j) return;            // n_j: a multiple of 8
+  const int pieces = (s_slot[e + 1] - s_slot[e]) / (it * jt);
+  const int64_t slot_size = static_cast<int64_t>(p.slot_i) * p.slot_j;
+  const int64_t stride = it * jt * slot_size;
+  const float* src = p.parts + (s_slot[e] + local) * slot_size + static_cast<int64_t>(i0) * p.slot_j + jj;
+  O* out = static_cast<O*>(p.out) +
+           ((FORM == kWgrad ? static_cast<int64_t>(e) * p.n_i : static_cast<int64_t>(s_off[e])) + i * h + i0) * p.n_j +
+           j * TM + jj;
+  float4 sum[V];
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    sum[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if constexpr (OUT == MOE_ELEM_F32)
+      if (FORM == kWgrad && p.accumulate && i0 + r * kJoinRows < ni)
+        sum[r] = *reinterpret_cast<const float4*>(out + static_cast<int64_t>(r * kJoinRows) * p.n_j);
+  }
+  for (int q = 0; q < pieces; q += U) {
+    float4 v[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < V; ++r)
+        v[u][r] = q + u < pieces && i0 + r * kJoinRows < ni
+                      ? *reinterpret_cast<const float4*>(src + (q + u) * stride + r * kJoinRows * p.slot_j)
+                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        sum[r].x += v[u][r].x;
+        sum[r].y += v[u][r].y;
+        sum[r].z += v[u][r].z;
+        sum[r].w += v[u][r].w;
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < V; ++r) {
+    if (i0 + r * kJoinRows >= ni) continue;
+    O* dst = out + static_cast<int64_t>(r * kJoinRows) * p.n_j;
+    if constexpr (OUT == MOE_ELEM_F32) {
+      *reinterpret_cast<float4*>(dst) = sum[r];
+    } else {
+      const O w[4] = {Elem<OUT>::from(sum[r].x), Elem<OUT>::from(sum[r].y), Elem<OUT>::from(sum[r].z),
+                      Elem<OUT>::from(sum[r].w)};
+      *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(w);
+    }
+  }
+}
+
+template <int FORM, int OUT>
+__global__ void __launch_bounds__(256, 2) join_pieces_kernel(const JoinParams p) {
+  extern __shared__ int s_tables[];
+  __shared__ int s_piece, s_bad;
+  int* s_off = s_tables;
+  int* s_tile = s_off + (p.E + 1);
+  int* s_slot = s_tile + (p.E + 1);
+  pdl_wait();
+  pdl_trigger();
+  if (*p.cut == 0) return;                                 // no tile in pieces
+  if (threadIdx.x < 32) build_split_tables<FORM, true>(p, s_off, s_tile, s_slot, &s_piece, &s_bad);
+  __syncthreads();
+  const int tiles = s_tile[p.E];
+  const int wide = (p.slot_i + 4 * kJoinRows - 1) / (4 * kJoinRows), steps = (p.slot_i + kJoinRows - 1) / kJoinRows;
+  if (tiles * steps > static_cast<int>(gridDim.x)) {
+    for (int x = blockIdx.x; x < tiles * wide; x += gridDim.x)
+      join_step<FORM, OUT, 4>(p, x, wide, s_off, s_tile, s_slot);
+  } else if (static_cast<int>(blockIdx.x) < tiles * steps) {
+    join_step<FORM, OUT, 1>(p, blockIdx.x, steps, s_off, s_tile, s_slot);
   }
 }
 
@@ -785,22 +1075,24 @@ bool encode(CUtensorMap* m, const void* base, int elem, int64_t cols, int64_t ro
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FORM, int OUT>
+template <int FORM, int OUT, bool SPLIT>
 cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
-  p.stages = Smem::bytes(p.E, STAGES) <= kMaxSmem ? STAGES : STAGES - 1;
-  const int smem = Smem::bytes(p.E, p.stages);
+  p.stages = Smem::bytes(p.E, STAGES, SPLIT) <= kMaxSmem ? STAGES : STAGES - 1;
+  const int smem = Smem::bytes(p.E, p.stages, SPLIT);
   static std::atomic<int> configured[64];
   int dev = 0;
   cudaGetDevice(&dev);
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || configured[dev].load(std::memory_order_relaxed) == 0) {
-    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM, OUT>,
+    const cudaError_t e = cudaFuncSetAttribute(grouped_matmul_kernel<FORM, OUT, SPLIT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     if (cached) configured[dev].store(1, std::memory_order_relaxed);
   }
   int64_t units = num_sms / 2;
-  if (max_tiles < units) units = max_tiles > 0 ? max_tiles : 1;
+  if (SPLIT) units = std::min<int64_t>(units, kSplitUnits);
+  else if (max_tiles < units) units = max_tiles > 0 ? max_tiles : 1;
+  p.units = static_cast<int>(units);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * units), 1, 1);
   cfg.blockDim = dim3(num_threads(FORM), 1, 1);
@@ -815,20 +1107,77 @@ cudaError_t launch_form(ProductParams p, int64_t max_tiles, int num_sms, cudaStr
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM, OUT>, p);
+  return cudaLaunchKernelEx(&cfg, grouped_matmul_kernel<FORM, OUT, SPLIT>, p);
+}
+
+template <int FORM, int OUT>
+cudaError_t launch_split(const ProductParams& p, float* parts, int num_sms, cudaStream_t stream) {
+  const cudaError_t e = launch_form<FORM, OUT, true>(p, 0, num_sms, stream);
+  if (e != cudaSuccess) return e;
+  JoinParams q{};
+  static_cast<Shape&>(q) = p;
+  q.units = std::min(num_sms / 2, kSplitUnits);
+  q.parts = parts;
+  q.out = p.out;
+  const size_t smem = sizeof(int) * 3 * (static_cast<size_t>(p.E) + 1);
+  return launch_chained(join_pieces_kernel<FORM, OUT>, dim3(static_cast<unsigned>(2 * num_sms)), dim3(256), smem, stream, q);
 }
 
 template <int OUT>
-cudaError_t launch_out(int form, const ProductParams& p, int64_t max_tiles, int num_sms, cudaStream_t stream) {
-  return form == kForward ? launch_form<kForward, OUT>(p, max_tiles, num_sms, stream)
-         : form == kDgrad ? launch_form<kDgrad, OUT>(p, max_tiles, num_sms, stream)
-                          : launch_form<kWgrad, OUT>(p, max_tiles, num_sms, stream);
+cudaError_t launch_out(int form, const ProductParams& p, float* parts, int64_t max_tiles, int num_sms,
+                       cudaStream_t stream) {
+  if (parts != nullptr)
+    return form == kForward ? launch_split<kForward, OUT>(p, parts, num_sms, stream)
+           : form == kDgrad ? launch_split<kDgrad, OUT>(p, parts, num_sms, stream)
+                            : launch_split<kWgrad, OUT>(p, parts, num_sms, stream);
+  return form == kForward ? launch_form<kForward, OUT, false>(p, max_tiles, num_sms, stream)
+         : form == kDgrad ? launch_form<kDgrad, OUT, false>(p, max_tiles, num_sms, stream)
+                          : launch_form<kWgrad, OUT, false>(p, max_tiles, num_sms, stream);
+}
+
+// Slots of a product whose tiles may be cut along r.  Cutting needs a second
+// launch, 2 us where nothing is cut and 4 to 6 us where something is; 64 of r
+// take a pair 0.27 us.  So it is for
+//   forward, dgrad  as many groups as rows allow leave half of the pairs without
+//                   a tile, and r has at least 48 blocks (256 rows, n = 2560 to
+//                   256 columns 22 us cut, 24 whole; n = 2048 21 both ways)
+//   wgrad           groups of even length leave half of the pairs without a tile
+//                   and have 48 blocks each (4096 rows, 256 x 256: 22 us cut, 31
+//                   whole; 2048 rows 22 both ways), or kSkewedRows rows,
+//                   few tiles a group, and possibly most rows in one group
+//                   (16 groups of 32768 rows, 512 x 512: even 31 us cut, 29 whole;
+//                   longest 9592 rows 45 and 57.  64 of 65536: even 47 and
+//                   45, all rows in one 59 and 305)
+struct Slots { int count, i, j; };
+Slots split_slots(int form, int64_t rows, int E, int n, int k) {
+  constexpr int64_t kMinBlocks = 6 * kMinPiece;
+  const int n_j = form == kForward ? n : k;
+  const int64_t jt = tiles_over(n_j, TM);
+  bool cut;
+  if (form == kWgrad) {
+    const int64_t tiles = tiles_over(n, TN) * jt;
+    cut = (2 * tiles * E <= kSplitUnits && ceil_div(rows, BK) >= kMinBlocks * E) ||
+          (4 * tiles <= kSplitUnits && rows >= kSkewedRows);
+  } else {
+    const int64_t tiles = std::max<int64_t>(std::min<int64_t>(rows, E), ceil_div(rows, TN)) * jt;
+    cut = rows > 0 && 2 * tiles <= kSplitUnits && tiles_over(form == kForward ? k : n, BK) >= kMinBlocks;
+  }
+  if (!cut) return {0, 0, 0};
+  const int64_t i_side = form == kWgrad ? n : std::min<int64_t>(rows, TN);
+  return {2 * kSplitUnits, even_height(static_cast<int>(i_side)), std::min<int>(TM, (n_j + 31) & ~31)};
+}
+size_t slots_bytes(const Slots& s) {
+  return sizeof(float) * static_cast<size_t>(s.count) * static_cast<size_t>(s.i) * static_cast<size_t>(s.j);
 }
 
 }  // namespace
 
 bool grouped_matmul_sm100_takes(const GroupedProduct& g) {
   return g.dtype != MOE_ELEM_F32 && g.n % 8 == 0 && g.k % 8 == 0;
+}
+
+size_t grouped_matmul_sm100_parts_bytes(const GroupedProduct& g, int form) {
+  return grouped_matmul_sm100_takes(g) ? slots_bytes(split_slots(form, g.rows, g.E, g.n, g.k)) : 0;
 }
 
 cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cudaStream_t stream,
@@ -871,10 +1220,19 @@ cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cu
       ok = ok && encode(&p.tmN[x], g.p, g.dtype, red, rows, 0, BK, 128 >> x, kIn);
     max_tiles = (ceil_div(g.rows, TN) + g.E) * tiles_over(p.n_j, TM);
   }
+  const Slots slots = split_slots(g.form, g.rows, g.E, g.n, g.k);
+  float* parts = slots.count > 0 ? g.parts : nullptr;
+  if (parts != nullptr) {
+    p.slot_i = slots.i;
+    p.slot_j = slots.j;
+    p.cut = g.status + kCutWord;
+    ok = ok && encode(&p.tmParts, parts, MOE_ELEM_F32, slots.j, static_cast<int64_t>(slots.count) * slots.i, 1, 32, 32,
+                      CU_TENSOR_MAP_SWIZZLE_NONE);
+  }
   if (!ok) { *map_error = true; return cudaErrorInvalidValue; }
-  return f32                              ? launch_out<MOE_ELEM_F32>(g.form, p, max_tiles, num_sms, stream)
-         : g.out_dtype == MOE_ELEM_F16    ? launch_out<MOE_ELEM_F16>(g.form, p, max_tiles, num_sms, stream)
-                                          : launch_out<MOE_ELEM_BF16>(g.form, p, max_tiles, num_sms, stream);
+  return f32                              ? launch_out<MOE_ELEM_F32>(g.form, p, parts, max_tiles, num_sms, stream)
+         : g.out_dtype == MOE_ELEM_F16    ? launch_out<MOE_ELEM_F16>(g.form, p, parts, max_tiles, num_sms, stream)
+                                          : launch_out<MOE_ELEM_BF16>(g.form, p, parts, max_tiles, num_sms, stream);
 }
 
 }  // namespace moe

@@ -125,12 +125,14 @@ struct GroupedProduct {
   void* out;
   int accumulate;           // kWgrad, fp32 output
   int32_t* status;
+  float* parts;             // grouped_matmul_sm100_parts_bytes() of workspace
 };
 // grouped_matmul_simt.cu (CUDA cores: fp32 operands, and sizes TMA cannot take)
 cudaError_t launch_grouped_matmul_simt(const GroupedProduct& g, int num_sms, cudaStream_t stream);
 // grouped_matmul_sm100.cu (tensor cores: 16-bit operands whose rows are whole
 // 16-byte vectors)
 bool grouped_matmul_sm100_takes(const GroupedProduct& g);
+size_t grouped_matmul_sm100_parts_bytes(const GroupedProduct& g, int form);
 cudaError_t launch_grouped_matmul_sm100(const GroupedProduct& g, int num_sms, cudaStream_t stream,
                                         bool* map_error);
 

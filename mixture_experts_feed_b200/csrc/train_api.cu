@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "inkling_moe.h"
 #include "internal.h"
@@ -32,6 +34,17 @@ moe_status_t check_grouped(const moe_grouped_desc_t* d) {
   return MOE_OK;
 }
 
+GroupedProduct grouped_sizes(const moe_grouped_desc_t* d) {
+  GroupedProduct g{};
+  g.rows = d->rows;
+  g.E = d->n_groups;
+  g.n = d->n;
+  g.k = d->k;
+  g.dtype = d->dtype;
+  g.out_dtype = d->out_dtype;
+  return g;
+}
+
 moe_status_t run_grouped(const moe_grouped_desc_t* d, int form, const void* p, const void* q,
                          const int32_t* offsets, void* out, int accumulate, void* ws,
                          size_t ws_bytes, void* stream) {
@@ -43,22 +56,17 @@ moe_status_t run_grouped(const moe_grouped_desc_t* d, int form, const void* p, c
   if (d->rows > 0 && !aligned16(p)) return MOE_ERR_INVALID_ARG;
   if ((form != kWgrad || d->rows > 0) && !aligned16(q)) return MOE_ERR_INVALID_ARG;
   if (!aligned4(offsets) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-  st = check_workspace(ws, ws_bytes, kStatusBytes);
-  if (st != MOE_OK) return st;
-  GroupedProduct g{};
+  GroupedProduct g = grouped_sizes(d);
   g.form = form;
-  g.rows = d->rows;
-  g.E = d->n_groups;
-  g.n = d->n;
-  g.k = d->k;
-  g.dtype = d->dtype;
-  g.out_dtype = d->out_dtype;
+  st = check_workspace(ws, ws_bytes, kStatusBytes + grouped_matmul_sm100_parts_bytes(g, form));
+  if (st != MOE_OK) return st;
   g.p = p;
   g.q = q;
   g.offsets = offsets;
   g.out = out;
   g.accumulate = accumulate ? 1 : 0;
   g.status = static_cast<int32_t*>(ws);
+  g.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!grouped_matmul_sm100_takes(g)) return cuda_status(launch_grouped_matmul_simt(g, device_sm_count(), s));
   bool map_error = false;
@@ -141,7 +149,11 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* 
   const moe_status_t st = check_grouped(desc);
   if (st != MOE_OK) return st;
   if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
-  *bytes = kStatusBytes;
+  const GroupedProduct g = grouped_sizes(desc);
+  size_t parts = 0;
+  for (const int form : {kForward, kDgrad, kWgrad})
+    parts = std::max(parts, grouped_matmul_sm100_parts_bytes(g, form));
+  *bytes = kStatusBytes + parts;
   return MOE_OK;
 }
 

@@ -89,6 +89,25 @@ def test_grouped_group_sizes(form, sizes):
     check_grouped(form, sizes, 264, 328, BF, BF, pad=5)
 
 
+# weight gradients of few tiles and many rows, input gradients and forward
+# products of few tiles and long sums: cut along the sum
+@pytest.mark.parametrize("sizes", [[0, 20000, 0], [4073], [10000, 1, 0, 7000, 3],
+                                   [0] * 300 + [16001, 500] + [0] * 9, [0, 64 * 74 * 8 + 65], [409] * 40, [2500]])
+@pytest.mark.parametrize("n,k", [(8, 8), (136, 264), (520, 40), (256, 256)])
+@pytest.mark.parametrize("dtype,out,accumulate", [(BF, BF, False), (HF, F32, False), (BF, F32, True), (HF, HF, False)])
+def test_wgrad_cut_along_the_rows(sizes, n, k, dtype, out, accumulate):
+    check_grouped("wgrad", sizes, n, k, dtype, out, pad=37, accumulate=accumulate)
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 7, 0, 2], [31, 33], [200, 0, 1], [700]])
+@pytest.mark.parametrize("wide,deep", [(8, 4096), (136, 4000), (264, 6152), (1000, 2056)])
+@pytest.mark.parametrize("form", ["forward", "dgrad"])
+@pytest.mark.parametrize("dtype,out", [(BF, BF), (HF, F32), (HF, HF), (BF, F32)])
+def test_products_cut_along_the_sum(form, sizes, wide, deep, dtype, out):
+    n, k = (wide, deep) if form == "forward" else (deep, wide)
+    check_grouped(form, sizes, n, k, dtype, out, pad=5)
+
+
 @pytest.mark.parametrize("form", ["forward", "dgrad"])
 @pytest.mark.parametrize("sizes", [[1], [3, 0, 9, 8, 0, 1], [64], [0, 50], [63]])
 @pytest.mark.parametrize("n,k", [(64, 128), (33, 51), (200, 4), (7, 260)])
@@ -202,6 +221,67 @@ def test_grouped_bad_offsets_are_recorded():
     # read as [0, 12, 20]
     ref, mag, m = th.grouped_exact("forward", p, q, torch.tensor([0, 12, 20]), o)
     th.check(o, ref, th.grouped_bound(ref, mag, m, BF), "clamped offsets")
+
+
+def test_grouped_bad_offsets_of_a_cut_product():
+    G, p, q, off, o = grouped_inputs("wgrad", [9000, 9000], 64, 72, BF, F32)
+    ws = moe.new_grouped_workspace(G)
+    assert ws.numel() > 256
+    bad = torch.tensor([0, 17000, 1 << 30], dtype=torch.int32, device="cuda")
+    moe.moe_grouped_matmul_wgrad(G, p, q, bad, o, ws)
+    with pytest.raises(moe.MoEError):
+        moe.read_device_status(ws)
+    ref, mag, m = th.grouped_exact("wgrad", p, q, torch.tensor([0, 17000, 18000]), o)
+    th.check(o, ref, th.grouped_bound(ref, mag, m, F32), "clamped offsets")
+
+
+def test_cut_products_in_a_graph():
+    """A forward product, its gradients and an accumulation, all cut, over one
+    workspace: captured and replayed with other rows and other group lengths."""
+    R, E, n, k = 20000, 5, 64, 4104
+    G, GF = moe.GroupedMatmul(R, E, n, k, BF), moe.GroupedMatmul(200, E, n, k, BF)
+    GD, GW = moe.GroupedMatmul(200, E, k, n, BF, F32), moe.GroupedMatmul(R, E, n, 136, BF, F32)
+    ws = max((moe.new_grouped_workspace(g) for g in (G, GF, GD, GW)), key=torch.Tensor.numel)
+    mk = lambda *s: torch.randn(*s, device="cuda").to(BF)   # noqa: E731
+    st = dict(x=mk(200, k), w=mk(E, n, k), w2=mk(E, k, n), d=mk(R, n), a=mk(R, 136))
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off_few = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    mko = lambda: (torch.zeros(200, n, dtype=BF, device="cuda"), torch.zeros(200, n, device="cuda"),   # noqa: E731
+                   torch.zeros(E, n, 136, device="cuda"))
+
+    def step(o, ws):
+        moe.moe_grouped_matmul(GF, st["x"], st["w"], off_few, o[0], ws)
+        moe.moe_grouped_matmul_dgrad(GD, st["x"], st["w2"], off_few, o[1], ws)
+        moe.moe_grouped_matmul_wgrad(GW, st["d"], st["a"], off, o[2], ws)
+        moe.moe_grouped_matmul_wgrad(GW, st["d"], st["a"], off, o[2], ws, accumulate=True)
+
+    o = mko()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(o, ws)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(o, ws)
+    for sizes in ([0, 19000, 0, 600, 3], [4000] * 5, [0] * 5, [1, 2, 3, 4, 5]):
+        for t in st.values():
+            t.copy_(torch.randn(t.shape, device="cuda"))
+        off[1:].copy_(torch.tensor(sizes).cumsum(0))
+        off_few[1:].copy_(torch.tensor(sizes).cumsum(0).clamp(max=200))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert moe.read_device_status(ws) == 0
+        ref, mag, m = th.grouped_exact("wgrad", st["d"], st["a"], off, o[2])
+        th.check(o[2], 2 * ref, 2 * th.grouped_bound(ref, mag, m + 1, F32), f"dW {sizes}")
+        live = int(off_few[-1])
+        for got, form, w, dt in ((o[0], "forward", st["w"], BF), (o[1], "dgrad", st["w2"], F32)):
+            ref, mag, m = th.grouped_exact(form, st["x"], w, off_few, got)
+            th.check(got[:live], ref[:live], th.grouped_bound(ref, mag, m, dt)[:live], f"{form} {sizes}")
+        o2 = mko()
+        step(o2, torch.cat([ws[:256], torch.empty_like(ws[256:])]))
+        for x, y in zip(o, o2):
+            assert torch.equal(x[:live], y[:live])
 
 
 def test_grouped_output_past_2_to_31_elements():

@@ -71,6 +71,23 @@ def test_grouped_workspace_size():
     assert moe.LIB.moe_grouped_workspace_size(grouped(E=0), ctypes.byref(n)) == INVALID
 
 
+def test_grouped_workspace_of_products_cut_along_the_sum():
+    """Few tiles and a long sum: the workspace holds the pieces, whatever the
+    output's type, and a smaller one is refused."""
+    ok = [FAKE] * 4
+    for shape in (dict(rows=8192, E=1, n=256, k=256), dict(rows=40000, E=64, n=512, k=512),
+                  dict(rows=32, E=1, n=64, k=4096), dict(rows=32, E=1, n=4096, k=64)):
+        for dt in (torch.bfloat16, torch.float16):
+            size = moe.grouped_workspace_size(moe.GroupedMatmul(dtype=dt, **shape))
+            assert 256 < size < 1 << 26
+            assert moe.grouped_workspace_size(moe.GroupedMatmul(dtype=dt, out_dtype=torch.float32, **shape)) == size
+        assert moe.grouped_workspace_size(moe.GroupedMatmul(dtype=torch.float32, **shape)) == 256
+        d = ctypes.byref(moe.GroupedMatmul(**shape).desc())
+        assert WORKSPACE in [f(d, *ok, FAKE, size - 1, None) for f in CALLS if f is not None]
+    assert moe.grouped_workspace_size(moe.GroupedMatmul(24576, 64, 2048, 2048)) == 256
+    assert moe.grouped_workspace_size(moe.GroupedMatmul(64, 64, 4096, 2048)) == 256
+
+
 def swiglu_call(name, rows=64, I=32, dtype=moe.MOE_BF16, E=4, off=FAKE, slot=FAKE, w=FAKE, ptrs=None,
                 ws=FAKE, nbytes=BIG):
     f = getattr(moe.LIB, name)
