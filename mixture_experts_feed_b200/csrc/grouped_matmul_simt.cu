@@ -31,14 +31,18 @@
 namespace moe {
 namespace {
 
-constexpr int TR = 16, NT = 256;
+constexpr int NT = 256;
+// r of a step
+__host__ __device__ constexpr int step_r(int tb) { return tb == 32 ? 64 : 16; }
 
 __device__ __forceinline__ float elem_f32(float v) { return v; }
 __device__ __forceinline__ float elem_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float elem_f32(__half v) { return __half2float(v); }
 template <typename O> __device__ __forceinline__ O elem_from(float v);
 template <> __device__ __forceinline__ float elem_from<float>(float v) { return v; }
-template <> __device__ __forceinline__ __nv_bfloat16 elem_from<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 elem_from<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
 template <> __device__ __forceinline__ __half elem_from<__half>(float v) { return __float2half_rn(v); }
 
 // Four consecutive elements; `vec`: 16-byte (fp32) or 8-byte aligned.
@@ -49,20 +53,32 @@ template <typename T> __device__ __forceinline__ float4 load4(const T* p) {
 }
 template <> __device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
+template <typename O> __device__ __forceinline__ void store4(O* p, float4 v) {
+  const O t[4] = {elem_from<O>(v.x), elem_from<O>(v.y), elem_from<O>(v.z), elem_from<O>(v.w)};
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
+}
+template <> __device__ __forceinline__ void store4<float>(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
 // One operand's tile of TB x TR, as M[x0 + x, r0 + r] with zeros outside
 // nx x nr.  RED: r contiguous (element x * ld + r), else x contiguous
-// (r * ld + x).  A thread carries TB / 64 groups of 4 elements from global
+// (r * ld + x).  A thread carries G groups of 4 elements from global
 // memory (fetch) to shared memory (place: tile[r][x]).
 template <bool RED, int TB, typename T> struct Operand {
-  static constexpr int G = TB / 64;
+  static constexpr int TR = step_r(TB), G = TB * TR / (4 * NT);
   const T* m;
   int64_t ld, x0, nx, nr;
   bool vec;
   float4 v[G];
   __device__ __forceinline__ void where(int g, int& x, int& r) const {
     const int i = static_cast<int>(threadIdx.x) + g * NT;
-    x = RED ? i >> 2 : (i % (TB / 4)) * 4;
-    r = RED ? (i & 3) * 4 : i / (TB / 4);
+    if (RED && TB == 32) {               // a warp: 8 of x, 16 of r (two lanes a bank in place())
+      const int lane = i & 31, run = i >> 5;
+      x = (run & 3) * 8 + (lane >> 2);
+      r = ((run >> 2) * 4 + (lane & 3)) * 4;
+      return;
+    }
+    x = RED ? i / (TR / 4) : (i % (TB / 4)) * 4;
+    r = RED ? (i % (TR / 4)) * 4 : i / (TB / 4);
   }
   __device__ __forceinline__ void fetch(int64_t r0) {
 #pragma unroll
@@ -110,7 +126,7 @@ struct SimtProduct {
 
 template <int FORM, int TB, typename T, typename O>
 __global__ void __launch_bounds__(NT, TB == 64 ? 3 : 2) grouped_matmul_simt_kernel(const SimtProduct g) {
-  constexpr int M = TB / 16;             // outputs a thread, each way
+  constexpr int M = TB / 16, TR = step_r(TB);   // outputs a thread, each way
   __shared__ __align__(16) float Ps[2][TR][TB + 4];
   __shared__ __align__(16) float Qs[2][TR][TB + 4];
   __shared__ int s_bad;
@@ -229,6 +245,149 @@ __global__ void __launch_bounds__(NT, TB == 64 ? 3 : 2) grouped_matmul_simt_kern
         const int64_t j = j0 + tx * 4 + 64 * (b / 4) + b % 4;
         if (j < cols) out[i * cols + j] = elem_from<O>(v[b]);
       }
+    }
+  }
+}
+
+// Tiles of 32 x 32 outputs, 64 of r at a time, of which every warp takes eight:
+// a lane sums 4 x 8 outputs over its warp's part of r, the eight warps' sums are
+// added at the end, in order.  Four times the tiles and a quarter of the steps of
+// TB = 64 (and 4 loads in flight a thread), for twice its operand bytes: faster
+// where 64 x 64 tiles do not fill the SMs (us, against them): dW of 2048 rows, 128 x 128,
+// 33 / 98; of 2048 rows, 640 x 640 (100 tiles), 68 / 92; 500 rows of 8 experts,
+// n = 1024, k = 256, input gradient 23 / 56.  With more of them: 2048 rows
+// of 16 experts, n = k = 512 (256 tiles), 61 / 44.  Bound by latency.
+template <int FORM, typename T, typename O>
+__global__ void __launch_bounds__(NT, 2) grouped_matmul_sliced_kernel(const SimtProduct g) {
+  constexpr int TB = 32, TR = step_r(TB), W = NT / 32;
+  using Tile = float[TR][TB + 4];
+  __shared__ __align__(16) Tile s_ops[4];              // P and Q, two buffers each; then the warps' sums
+  static_assert(sizeof(s_ops) == sizeof(float) * W * TB * (TB + 4), "the sums take the operands' place");
+  float (*s_sum)[TB][TB + 4] = reinterpret_cast<float (*)[TB][TB + 4]>(&s_ops[0][0][0]);
+  __shared__ int s_bad;
+  extern __shared__ int s_tables[];
+  int* s_off = s_tables;
+  int* s_tile = s_tables + g.E + 1;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int cols = FORM == kForward ? g.n : g.k;
+  const int j_tiles = (cols + TB - 1) / TB;
+  const int i_tiles = (g.n + TB - 1) / TB;
+  if (tid == 0) s_bad = 0;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  if (tid < 32)
+    build_tile_prefix(g.offsets, g.E, 0, 0, kAllTiles, TB, j_tiles, g.rows_cap, s_off, s_tile, &s_bad);
+  __syncthreads();
+  if (tid == 0 && s_bad) record_status(g.status, DEV_BAD_ROW);
+  const int64_t total = FORM == kWgrad ? static_cast<int64_t>(g.E) * i_tiles * j_tiles : s_tile[g.E];
+  const int tx = tid & 3, ty = (tid & 31) >> 2;
+
+  for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    int e, it, jt;
+    if (FORM == kWgrad) {
+      e = static_cast<int>(tile / (static_cast<int64_t>(i_tiles) * j_tiles));
+      const int local = static_cast<int>(tile - static_cast<int64_t>(e) * i_tiles * j_tiles);
+      it = local / j_tiles;
+      jt = local - it * j_tiles;
+    } else {
+      decode_tile(static_cast<int>(tile), s_tile, g.E, s_off, g.E, 0, kAllTiles, TB, e, it, jt);
+    }
+    const int64_t row0 = s_off[e];
+    const int rows = s_off[e + 1] - s_off[e];
+    if (FORM == kWgrad && g.accumulate && rows == 0) continue;
+    const T* P = static_cast<const T*>(g.p);
+    const T* Q = static_cast<const T*>(g.q);
+    const int64_t i0 = static_cast<int64_t>(it) * TB, j0 = static_cast<int64_t>(jt) * TB;
+    const int64_t ni = FORM == kWgrad ? g.n : rows;
+    const int64_t nr = FORM == kForward ? g.k : (FORM == kDgrad ? g.n : rows);
+    if (FORM == kWgrad) {
+      P += row0 * g.n;
+      Q += row0 * g.k;
+    } else {
+      P += row0 * (FORM == kForward ? g.k : g.n);
+      Q += static_cast<int64_t>(e) * g.n * g.k;
+    }
+    f32x2 acc[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[a][b] = 0;
+    Operand<FORM != kWgrad, TB, T> op{P, FORM == kForward ? g.k : g.n, i0, ni, nr, g.vec_p != 0};
+    Operand<FORM == kForward, TB, T> oq{Q, g.k, j0, cols, nr, g.vec_q != 0};
+    int buf = 0;
+    __syncthreads();                     // the previous tile's sums are read
+    if (nr > 0) {
+      op.fetch(0);
+      oq.fetch(0);
+      op.place(s_ops[0]);
+      oq.place(s_ops[2]);
+      __syncthreads();
+    }
+    for (int64_t r0 = 0; r0 < nr; r0 += TR) {
+      const bool more = r0 + TR < nr;
+      if (more) {
+        op.fetch(r0 + TR);
+        oq.fetch(r0 + TR);
+      }
+#pragma unroll
+      for (int x = 0; x < TR / W; ++x) {
+        const int r = warp * (TR / W) + x;
+        const float4 pv = *reinterpret_cast<const float4*>(&s_ops[buf][r][ty * 4]);
+        const ulonglong2 q0 = *reinterpret_cast<const ulonglong2*>(&s_ops[2 + buf][r][tx * 8]);
+        const ulonglong2 q1 = *reinterpret_cast<const ulonglong2*>(&s_ops[2 + buf][r][tx * 8 + 4]);
+        const float pa[4] = {pv.x, pv.y, pv.z, pv.w};
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const f32x2 p2 = pack2(pa[a], pa[a]);
+          acc[a][0] = fma2(p2, q0.x, acc[a][0]);
+          acc[a][1] = fma2(p2, q0.y, acc[a][1]);
+          acc[a][2] = fma2(p2, q1.x, acc[a][2]);
+          acc[a][3] = fma2(p2, q1.y, acc[a][3]);
+        }
+      }
+      if (more) {
+        op.place(s_ops[buf ^ 1]);
+        oq.place(s_ops[2 + (buf ^ 1)]);
+        __syncthreads();
+        buf ^= 1;
+      }
+    }
+    __syncthreads();                     // the last operands are read
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        *reinterpret_cast<ulonglong2*>(&s_sum[warp][ty * 4 + a][tx * 8 + 4 * b]) =
+            make_ulonglong2(acc[a][2 * b], acc[a][2 * b + 1]);
+    __syncthreads();
+    const int ii = tid >> 3, jj = (tid & 7) * 4;         // four outputs a thread
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float4 u = *reinterpret_cast<const float4*>(&s_sum[w][ii][jj]);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+    const int64_t left = i0 + ii < ni ? cols - (j0 + jj) : 0;
+    O* out = static_cast<O*>(g.out) +
+             ((FORM == kWgrad ? static_cast<int64_t>(e) * g.n : row0) + i0 + ii) * cols + j0 + jj;
+    if (left >= 4 && cols % 4 == 0) {
+      if (FORM == kWgrad && g.accumulate) {
+        const float4 old = load4(out);
+        v.x += old.x;
+        v.y += old.y;
+        v.z += old.z;
+        v.w += old.w;
+      }
+      store4(out, v);
+    } else {
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b < left) out[b] = elem_from<O>(FORM == kWgrad && g.accumulate ? f[b] + elem_f32(out[b]) : f[b]);
     }
   }
 }
@@ -434,6 +593,17 @@ cudaError_t launch_tile(const GroupedProduct& g, int num_sms, cudaStream_t strea
 }
 
 template <int FORM, typename T, typename O>
+cudaError_t launch_sliced(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
+  SimtProduct s{g.p, g.q, g.out, g.offsets, g.status, g.E, g.n, g.k, static_cast<int>(g.rows), g.accumulate, 0, 0};
+  s.vec_p = (FORM == kForward ? g.k : g.n) % 4 == 0;
+  s.vec_q = g.k % 4 == 0;
+  const size_t smem = sizeof(int) * (2 * static_cast<size_t>(g.E) + 2);
+  const unsigned grid = static_cast<unsigned>(
+      std::max<int64_t>(1, std::min<int64_t>(tile_bound<FORM>(g, 32), static_cast<int64_t>(num_sms) * 2)));
+  return launch_chained(grouped_matmul_sliced_kernel<FORM, T, O>, grid, NT, smem, stream, s);
+}
+
+template <int FORM, typename T, typename O>
 cudaError_t launch_few_rows(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
   SimtProduct s{g.p, g.q, g.out, g.offsets, g.status, g.E, g.n, g.k, static_cast<int>(g.rows), 0, 0, 0};
   s.vec_q = g.k % 4 == 0;
@@ -453,8 +623,12 @@ cudaError_t launch_form(const GroupedProduct& g, int num_sms, cudaStream_t strea
   // rows / 128 + E bounds the tiles from above by E: full tiles alone count
   const int64_t full = FORM == kWgrad ? tile_bound<FORM>(g, 128)
                                       : g.rows / 128 * ceil_div(FORM == kForward ? g.n : g.k, 128);
-  return full >= num_sms ? launch_tile<FORM, 128, T, O>(g, num_sms, stream)
-                         : launch_tile<FORM, 64, T, O>(g, num_sms, stream);
+  if (full >= num_sms) return launch_tile<FORM, 128, T, O>(g, num_sms, stream);
+  const int64_t tiles = FORM == kWgrad ? tile_bound<FORM>(g, 64)
+                                       : std::max<int64_t>(ceil_div(g.rows, 64), std::min<int64_t>(g.rows, g.E)) *
+                                             ceil_div(FORM == kForward ? g.n : g.k, 64);
+  return 4 * tiles < 3 * num_sms ? launch_sliced<FORM, T, O>(g, num_sms, stream)
+                                 : launch_tile<FORM, 64, T, O>(g, num_sms, stream);
 }
 
 template <typename T, typename O>

@@ -183,9 +183,10 @@ __device__ __forceinline__ void build_tables(const Shape& p, int* s_off, int* s_
 // group_blocks(e) blocks of r; in ceil(blocks / *s_piece) pieces of even
 // length.  Pieces are as long as every pair's share of all blocks, at least
 // kMinPiece, and a little longer where the pieces would otherwise make a
-// second round; nothing is cut for less than kMinGain blocks.  s_tile = exclusive prefix of the pieces (JOIN: of the tiles of
-// more than one piece), s_slot = exclusive prefix of the pieces of such tiles: fewer than
-// 2 x units, because every tile in pieces has more blocks than a pair's share.
+// second round; nothing is cut for less than kMinGain blocks.  s_tile =
+// exclusive prefix of the pieces (JOIN: of the tiles of more than one piece),
+// s_slot = exclusive prefix of the pieces of such tiles: fewer than 2 x units,
+// because every tile in pieces has more blocks than a pair's share.
 template <int FORM> __device__ __forceinline__ int group_tiles(const Shape& p, const int* s_off, int e) {
   return tiles_over(FORM == kWgrad ? p.n_i : s_off[e + 1] - s_off[e], TN) * tiles_over(p.n_j, TM);
 }
@@ -1120,7 +1121,8 @@ cudaError_t launch_split(const ProductParams& p, float* parts, int num_sms, cuda
   q.parts = parts;
   q.out = p.out;
   const size_t smem = sizeof(int) * 3 * (static_cast<size_t>(p.E) + 1);
-  return launch_chained(join_pieces_kernel<FORM, OUT>, dim3(static_cast<unsigned>(2 * num_sms)), dim3(256), smem, stream, q);
+  return launch_chained(join_pieces_kernel<FORM, OUT>, dim3(static_cast<unsigned>(2 * num_sms)), dim3(256), smem,
+                        stream, q);
 }
 
 template <int OUT>
