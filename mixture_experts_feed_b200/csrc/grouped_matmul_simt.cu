@@ -7,16 +7,18 @@
 //   dgrad    P = dout [R, n] (r contiguous), Q = W[e]        (j contiguous)
 //   wgrad    P = dout        (i contiguous), Q = a           (j contiguous)
 //
-// Tiles of TB x TB outputs, 16 of r at a time through shared memory in two
-// buffers (the next step's operands are in flight while this one is used), 256
-// threads with (TB / 16)^2 outputs each.  TB = 128 reads 64 bytes of shared
-// memory for 64 FMAs a thread and step, TB = 64 32 bytes for 16: the larger
-// tile where its tiles fill the SMs, the smaller one elsewhere.  Products
-// go two at a time (packed fp32 FMAs): the same rate from the FMA pipe for half
-// the issue slots, which the loads need.  The reduction
-// runs in one fixed order, so results repeat bit for bit.  Bound by shared
-// memory at TB = 64 (2048 rows, n = k = 640, fp32: 75 us) and by latency on
-// smaller batches; 2048 rows of 4 experts, n = k = 1024: dW 106 us (40 TFLOP/s).
+// Three kernels.  Tiles of TB x TB outputs, 16 of r at a time through shared
+// memory in two buffers (the next step's operands are in flight while this one
+// is used), 256 threads with (TB / 16)^2 outputs each: TB = 128 reads 64 bytes
+// of shared memory for 64 FMAs a thread and step, TB = 64 32 bytes for 16, the
+// larger tile where its tiles fill the SMs.  Where 64 x 64 tiles do not, or
+// would be half empty, tiles of 32 x 32 whose sum the block's warps share; and
+// for a handful of rows no tiles at all (below, with the figures of both).
+// Products go two at a time (packed fp32 FMAs): the same rate from the FMA pipe
+// for half the issue slots, which the loads need.  Every reduction runs in one
+// fixed order, so results repeat bit for bit.  Bound by shared memory at TB = 64
+// (2048 rows, n = k = 640, fp32: 75 us) and by latency on smaller batches; 2048
+// rows of 4 experts, n = k = 1024: dW 106 us (40 TFLOP/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -256,7 +258,9 @@ __global__ void __launch_bounds__(NT, TB == 64 ? 3 : 2) grouped_matmul_simt_kern
 // where 64 x 64 tiles do not fill the SMs (us, against them): dW of 2048 rows, 128 x 128,
 // 33 / 98; of 2048 rows, 640 x 640 (100 tiles), 68 / 92; 500 rows of 8 experts,
 // n = 1024, k = 256, input gradient 23 / 56.  With more of them: 2048 rows
-// of 16 experts, n = k = 512 (256 tiles), 61 / 44.  Bound by latency.
+// of 16 experts, n = k = 512 (256 tiles), 61 / 44.  Also for up to 32 rows an
+// expert: 128 rows of 8, n = k = 1024, 29 / 57; 1024 of 32, 98 / 157.  Bound by
+// latency.
 template <int FORM, typename T, typename O>
 __global__ void __launch_bounds__(NT, 2) grouped_matmul_sliced_kernel(const SimtProduct g) {
   constexpr int TB = 32, TR = step_r(TB), W = NT / 32;
@@ -398,15 +402,15 @@ __global__ void __launch_bounds__(NT, 2) grouped_matmul_sliced_kernel(const Simt
 //   forward  a warp per two n: its lanes walk k, then add up
 //   dgrad    a block per 32 k: eight lanes of 4 k each for a row of W, 32 rows of
 //            W at a time, then the 32 partial sums add up
-// Each sum has one fixed order.  fp32, against the tiles (us):
-//   3 rows of 17 experts, n = 1024, k = 520     forward 10 / 35, dgrad 12 / 55
-//   64 of 1, n = k = 1024                       forward 35 / 57, dgrad 25 / 53
-//   64 of 1, n = k = 4096                       forward 222 / 209, dgrad 199 / 199
-//   512 of 64, n = k = 1024                     forward 207 / 258, dgrad 156 / 246
-//   256 of 16 (16 each), n = k = 1024           forward 98 / 80, dgrad 88 / 76
-// so it takes the calls of up to 64 rows, or of up to 8 rows an expert.  Bound by
-// the loads of P from L1 where rows are eight and by latency below that (512 of 64: 1.3
-// and 1.7 TB/s of weights).
+// Each sum has one fixed order.  Against the 32 x 32 tiles, us:
+//   4 rows, n = k = 1024, fp32                  16 / 23, 8 rows 23 / 23
+//   128 rows of 64 experts, n = k = 1024, fp32  76 / 170
+//   256 of 64, n = k = 512, fp32                45 / 57, 512 rows 61 / 57
+//   32 rows, n = 1001, k = 999, bf16            forward 18 / 47, dgrad 35 / 49
+//   64 of 8, n = 1001, k = 999, bf16            forward 29 / 49, dgrad 39 / 51
+// so it takes calls of up to 4 rows an expert; where rows are no whole vectors,
+// whose elements the tiles fetch one by one, of up to 8 an expert or 64 in all.
+// Bound by the loads of P from L1 and by latency (128 of 64: 3.5 TB/s of weights).
 constexpr int kFewRows = 64;
 constexpr int kRowsAtOnce = 8;
 constexpr int kFewNs = 2;         // n of a warp of the forward product
@@ -617,9 +621,13 @@ cudaError_t launch_few_rows(const GroupedProduct& g, int num_sms, cudaStream_t s
 
 template <int FORM, typename T, typename O>
 cudaError_t launch_form(const GroupedProduct& g, int num_sms, cudaStream_t stream) {
-  if constexpr (FORM != kWgrad)
-    if (g.rows <= kFewRows || g.rows <= kRowsAtOnce * static_cast<int64_t>(g.E))
+  if constexpr (FORM != kWgrad) {
+    const int64_t E = g.E;
+    const bool vec = g.n % 4 == 0 && g.k % 4 == 0;
+    if (vec ? g.rows <= 4 * E : g.rows <= std::max<int64_t>(kFewRows, kRowsAtOnce * E))
       return launch_few_rows<FORM, T, O>(g, num_sms, stream);
+    if (g.rows <= 32 * E) return launch_sliced<FORM, T, O>(g, num_sms, stream);   // tiles of 64 half empty
+  }
   // rows / 128 + E bounds the tiles from above by E: full tiles alone count
   const int64_t full = FORM == kWgrad ? tile_bound<FORM>(g, 128)
                                       : g.rows / 128 * ceil_div(FORM == kForward ? g.n : g.k, 128);

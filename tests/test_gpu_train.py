@@ -116,6 +116,24 @@ def test_grouped_few_rows_on_the_cuda_cores(form, sizes, n, k, dtype):
     check_grouped(form, sizes, n, k + (dtype == BF), dtype, dtype, pad=64 - sum(sizes))
 
 
+# four rows an expert at most, and the rows at once around their limit
+@pytest.mark.parametrize("form", ["forward", "dgrad"])
+@pytest.mark.parametrize("sizes", [[1], [2], [3], [4], [2, 0, 0, 10], [0] * 40 + [17, 2, 1] + [0] * 5, [4] * 30])
+@pytest.mark.parametrize("n,k", [(64, 128), (36, 260), (1000, 4), (132, 1000)])
+def test_grouped_up_to_four_rows_an_expert(form, sizes, n, k):
+    check_grouped(form, sizes, n, k, F32, F32)
+
+
+# enough 64 x 64 tiles for every SM, and fewer full ones of 128
+@pytest.mark.parametrize("sizes,n,k", [([700, 0, 500, 300], 392, 332), ([1500], 333, 391), ([90, 1, 260, 700], 700, 321)])
+@pytest.mark.parametrize("form", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("dtype,out", [(F32, F32), (BF, BF), (HF, F32)])
+def test_grouped_many_tiles_on_the_cuda_cores(form, sizes, n, k, dtype, out):
+    check_grouped(form, sizes, n, k + (k % 8 == 0 and dtype != F32), dtype, out, pad=3)
+    if form == "wgrad" and out == F32:
+        check_grouped(form, sizes, n, k + (k % 8 == 0 and dtype != F32), dtype, out, pad=3, accumulate=True)
+
+
 @pytest.mark.parametrize("sizes", [RAGGED, [0, 0], [3000, 0, 1]])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_wgrad_accumulates(sizes, dtype):
