@@ -489,7 +489,9 @@ typedef struct {
  * Its head is the status word: initialise it once with moe_workspace_init().
  * 256 bytes, and up to 39 MB more for the sizes whose products may be cut
  * along the sum (few output tiles and a long sum; see below): partial sums,
- * with nothing in them to initialise or to keep. */
+ * with nothing in them to initialise or to keep.  With less (256 bytes at
+ * least, else MOE_ERR_WORKSPACE) the same products run uncut: any initialised
+ * workspace of this library will do. */
 moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* bytes);
 
 /*
@@ -504,7 +506,8 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* 
  * they hold (NaN too) reaches no result.  An expert without rows gets
  * dW[e] = 0.  With accumulate != 0 (out_dtype MOE_ELEM_F32 only, else
  * MOE_ERR_INVALID_ARG) dW[e] += dout_e^T @ a_e, and an expert without rows
- * keeps its dW[e].  Results are the same on every run.
+ * keeps its dW[e].  Results are the same on every run (those of a product that
+ * is cut differ from the uncut ones' in the order of their sums).
  * Offsets that decrease or leave [0, R] are recorded in the status word
  * (MOE_ERR_DEVICE_CHECK) and read as the nearest valid ones.
  * bf16 and fp16 operands with n % 8 == 0 and k % 8 == 0 run on the tensor

@@ -656,7 +656,7 @@ def new_grouped_workspace(G: GroupedMatmul, device=None, stream=None) -> torch.T
     """Allocate (with torch) and initialise a workspace for the product ``G``
     and its two gradients (256 bytes; up to 39 MB where they may be cut along
     a long sum).  One workspace of the largest size serves products that run
-    one after the other."""
+    one after the other; in a smaller one they run uncut."""
     return _new_workspace(grouped_workspace_size(G), device, stream)
 
 

@@ -125,7 +125,7 @@ struct GroupedProduct {
   void* out;
   int accumulate;           // kWgrad, fp32 output
   int32_t* status;
-  float* parts;             // grouped_matmul_sm100_parts_bytes() of workspace
+  float* parts;             // grouped_matmul_sm100_parts_bytes() of workspace, or null: no tile is cut
 };
 // grouped_matmul_simt.cu (CUDA cores: fp32 operands, and sizes TMA cannot take)
 cudaError_t launch_grouped_matmul_simt(const GroupedProduct& g, int num_sms, cudaStream_t stream);

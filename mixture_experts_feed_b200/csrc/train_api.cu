@@ -58,15 +58,17 @@ moe_status_t run_grouped(const moe_grouped_desc_t* d, int form, const void* p, c
   if (!aligned4(offsets) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
   GroupedProduct g = grouped_sizes(d);
   g.form = form;
-  st = check_workspace(ws, ws_bytes, kStatusBytes + grouped_matmul_sm100_parts_bytes(g, form));
+  st = check_workspace(ws, ws_bytes, kStatusBytes);
   if (st != MOE_OK) return st;
+  // a workspace of another product, or of the layer, may be too small for the pieces: uncut then
+  if (ws_bytes - kStatusBytes >= grouped_matmul_sm100_parts_bytes(g, form))
+    g.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   g.p = p;
   g.q = q;
   g.offsets = offsets;
   g.out = out;
   g.accumulate = accumulate ? 1 : 0;
   g.status = static_cast<int32_t*>(ws);
-  g.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!grouped_matmul_sm100_takes(g)) return cuda_status(launch_grouped_matmul_simt(g, device_sm_count(), s));
   bool map_error = false;

@@ -253,6 +253,21 @@ def test_grouped_bad_offsets_of_a_cut_product():
     th.check(o, ref, th.grouped_bound(ref, mag, m, F32), "clamped offsets")
 
 
+def test_products_in_a_smaller_workspace_run_uncut():
+    for form, sizes, n, k in (("wgrad", [9000, 9000], 64, 72), ("forward", [40, 3], 64, 4096), ("dgrad", [40, 3], 4096, 64)):
+        G, p, q, off, o = grouped_inputs(form, sizes, n, k, BF, F32)
+        full = moe.grouped_workspace_size(G)
+        assert full > 256
+        ref, mag, m = th.grouped_exact(form, p, q, off, o)
+        for size in (256, full - 1, full):
+            ws = torch.zeros(full + 64, dtype=torch.uint8, device="cuda")
+            ws[size:] = 77
+            o.fill_(float("nan"))
+            run_grouped(form, G, p, q, off, o, ws[:size])
+            th.check(o, ref, th.grouped_bound(ref, mag, m, F32), f"{form} {size}")
+            assert bool((ws[size:] == 77).all())
+
+
 def test_cut_products_in_a_graph():
     """A forward product, its gradients and an accumulation, all cut, over one
     workspace: captured and replayed with other rows and other group lengths."""
