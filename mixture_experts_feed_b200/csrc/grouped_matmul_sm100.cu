@@ -376,11 +376,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
       __nanosleep(100);
     }
   }
-  return __shfl_sync(0xffffffffu, got, 0) != 0;
+  got = __shfl_sync(0xffffffffu, got, 0);
+  __syncwarp();                            // the shuffle alone orders no memory
+  return got != 0;
 }
 
 // mbar_wait by a whole warp that stays converged; `cluster`: with acquire at
-// cluster scope.
+// cluster scope, for what threads of the other CTA wrote to shared memory.
 __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
                                          bool cluster = false) {
   const bool got = cluster ? mbar_wait_cluster(bar, parity, abort, status) : mbar_wait(bar, parity, abort, status);
@@ -701,7 +703,7 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
           for (int b = b0; b < b1; ++b) {
             // a partial block (wgrad) has been mended by threads of both CTAs
             const bool partial = FORM == kWgrad && (b + 1) * BK > t.rows;
-            if (!all_wait(&full[stage], phase, s_abort, p.status)) { ok = false; break; }
+            if (!all_wait(&full[stage], phase, s_abort, p.status, partial)) { ok = false; break; }
             tc_fence_after();
             const uint64_t mdesc = mdesc0 + stage * next_stage, ndesc = ndesc0 + stage * next_stage;
             const int steps = partial ? (t.rows - b * BK + 15) >> 4 : BK / 16;
@@ -758,11 +760,10 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
       stage = (stage + t.blocks - 1) % stages;             // the last block's stage
       const int valid = t.rows - (t.blocks - 1) * BK;
       if (valid < BK) {
-        // this CTA's loads have landed: zero the rows past the group up to
-        // the next multiple of 16, in both operands
-        int got = 1;
-        if (lane == 0) got = mbar_wait(&tail[stage], (tail_par >> stage) & 1u, s_abort, p.status) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, got, 0)) break;
+        // this CTA's loads have landed (every lane waits, so that its stores
+        // follow them): zero the rows past the group up to the next multiple
+        // of 16, in both operands
+        if (!all_wait(&tail[stage], (tail_par >> stage) & 1u, s_abort, p.status)) break;
         tail_par ^= 1u << stage;
         uint8_t* base = smem + stage * STAGE_BYTES + valid * 128;
         const int count = (((valid + 15) & ~15) - valid) * 8;       // 16-byte pieces a box
@@ -770,9 +771,14 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         for (int box = 0; box < boxes; ++box)                       // M side's two, then N side's
           for (int x = lane; x < count; x += 32)
             *reinterpret_cast<uint4*>(base + box * 8192 + x * 16) = make_uint4(0, 0, 0, 0);
+        // The MMA that reads these zeros is issued by rank 0: each lane's stores
+        // are made visible to the async proxy, gathered by the warp's barrier, and
+        // released at cluster scope by the arrival that the issuer acquires.  The
+        // release covers shared memory alone: one over all memory waits for other
+        // warps' outputs too (24576 rows of 64 experts: 254 us against 230).
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&full[stage], 0));
+        if (lane == 0) mbar_arrive_cluster_smem(mapa_shared(&full[stage], 0));
       }
       stage = (stage + 1) % stages;
     }

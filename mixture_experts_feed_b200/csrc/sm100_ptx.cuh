@@ -258,12 +258,22 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same without the cluster-scope release, for signals that only order
-// tensor-memory accesses (tcgen05 fences do that): the release waits until
-// every earlier write of the thread is visible to the cluster (~2000 clocks
-// in a storing epilogue).
+// The same without the cluster-scope release: for signals that order
+// tensor-memory accesses alone (tcgen05 fences do that) or nothing at all,
+// never for data in shared memory.  The release waits until every earlier
+// write of the thread is visible to the cluster (~2000 clocks in a storing
+// epilogue).
 __device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// mbar_arrive_cluster for data in this CTA's shared memory alone: the release
+// at cluster scope covers what was written there (by this thread, or by
+// threads it has synchronised with) and waits for nothing else.
+__device__ __forceinline__ void mbar_arrive_cluster_smem(uint32_t cluster_addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
 }
 
 // try_wait with acquire at cluster scope: the waiter then sees what the
