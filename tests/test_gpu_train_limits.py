@@ -16,6 +16,8 @@ except ImportError:   # collected on CPU-only machines too; the gpu marker desel
     moe = None
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+CALL = {"forward": "moe_grouped_matmul", "dgrad": "moe_grouped_matmul_dgrad",
+        "wgrad": "moe_grouped_matmul_wgrad"}
 
 
 # ---------------------------------------------------------- grouped products
@@ -51,3 +53,42 @@ def test_wgrad_rows_of_neighbours_never_enter(out, accumulate):
         assert torch.equal(o[::2], first[::2])
     th.check(first[::2], ref[::2], th.grouped_bound(ref, mag, m, out)[::2], "finite groups")
     assert moe.read_device_status(ws) == 0
+
+
+def product(form, sizes, n, k, dtype, out, cut, values=torch.randn, accumulate=False, old=0.0, seed=1):
+    """(output, exact output) of a product.  `cut`: None for sizes that are never
+    cut along the sum; else the workspace holds the pieces (True) or does not."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    E, R = len(sizes), sum(sizes)
+    mk = lambda *s: values(*s, generator=g, device="cuda")   # noqa: E731
+    off = torch.tensor([0] + torch.tensor(sizes).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    p = mk(R, k if form == "forward" else n).to(dtype)
+    q = (mk(R, k) if form == "wgrad" else mk(E, n, k)).to(dtype)
+    o = mk(*((E, n, k) if form == "wgrad" else (R, n if form == "forward" else k))).to(out) * old
+    G = moe.GroupedMatmul(R, E, n, k, dtype, out)
+    full = moe.grouped_workspace_size(G)
+    assert (full > 256) == (cut is not None)
+    ws = moe.new_grouped_workspace(G)[:full if cut else 256]
+    ref = th.grouped_exact(form, p, q, off, o, accumulate)[0]
+    getattr(moe, CALL[form])(G, p, q, off, o, ws, **(dict(accumulate=True) if accumulate else {}))
+    torch.cuda.synchronize()
+    assert moe.read_device_status(ws) == 0
+    return o, ref
+
+
+LONG = [("forward", [300, 100], 256, 6144, True), ("forward", [300, 100], 256, 6144, False),
+        ("forward", [300, 100, 200, 50], 4096, 6144, None),
+        ("dgrad", [300, 100], 6144, 256, True), ("dgrad", [300, 100], 6144, 256, False),
+        ("wgrad", [9000, 500], 256, 264, True), ("wgrad", [9000, 500], 256, 264, False),
+        ("wgrad", [9000, 0], 2048, 2048, None)]
+
+
+@pytest.mark.parametrize("form,sizes,n,k,cut", LONG)
+def test_long_sums_in_fp32_are_added_in_short_chains(form, sizes, n, k, cut):
+    """A tensor-core accumulator truncates at each step of 16 terms: by half a
+    unit of 2^-23 on average, 32 times in a chain of 512 terms, so at most
+    16 x 2^-23 of the result's 2-norm if all of them added up (chains are
+    joined by additions that round).  One chain of 6144 terms is past 6e-6."""
+    o, ref = product(form, sizes, n, k, BF, F32, cut)
+    rel = float((o.double() - ref).norm() / ref.norm())
+    assert rel < 16 * 2.0 ** -23, rel
