@@ -30,14 +30,17 @@
 // zeros in shared memory, for both operands, and the MMA runs that many
 // 16-row steps.
 //
-// fp32 outputs: the accumulator truncates instead of rounding at every step,
-// an error that grows with the chain (random normal operands, 2-norm: 2.3e-7
-// for chains of 256 terms, 4.7e-7 for 512, 1.0e-6 for 1024, 6.7e-6 for 6144;
-// a library product in fp32 has 1.6e-7 to 6e-7).  One chain is kept to 512
-// terms (kChain blocks of 64), and the chains of a tile are added in fp32
-// registers by the warps that store it, in order: chains of 256 cost 6% on the
-// largest input gradient, 512 nothing.  16-bit outputs round away hundreds of
-// times more and take one chain.
+// The accumulator truncates instead of rounding at every step, an error that
+// grows with the chain and always leans toward zero (2-norm, random normal
+// operands: 2.3e-7 for chains of 256 terms, 4.7e-7 for 512, 1.0e-6 for 1024,
+// 6.7e-6 for 6144; a library product in fp32 has 1.6e-7 to 6e-7.  Products of
+// one sign: 3e-6 for 512, and 4.2e-4 for 65536, a whole half step of fp16).
+// One chain is kept to 512 terms (kChain blocks of 64), and the chains of a tile
+// are added in fp32 registers by the warps that store it, in order, for every
+// type of output.  Against one chain of any length that takes 1.5% more on 16-bit
+// forward products (24576 rows of 64 experts, 2048 x 2048: 223.7 us / 220.4) and
+// 1% on their weight gradients; chains of 256 cost 6% on the largest fp32 input
+// gradient.
 //
 // Few tiles with a long sum (the weight gradient of one large expert, a
 // product of few rows with a long k) would leave most pairs idle.  Such tiles are cut
@@ -100,7 +103,7 @@ constexpr int OUT_BYTES = 4096;          // staging of an epilogue warp (16-bit:
 constexpr uint32_t TMEM_COLS = 512;      // two accumulators of 256 columns
 constexpr int TQ = 8;                    // slots of the tile queue
 constexpr int kBand = 8;                 // i tiles per band (tile order)
-constexpr int kChain = 8;                // blocks of 64 per accumulation chain, fp32 outputs
+constexpr int kChain = 8;                // blocks of 64 per accumulation chain
 constexpr int kMaxSmem = 232448;         // shared memory a block can have
 constexpr int kSplitUnits = 74;          // CTA pairs that pieces are made for
 constexpr int kMinPiece = 8;             // blocks of 64 r of a piece, at least
@@ -501,8 +504,6 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_bad = reinterpret_cast<int*>(s_tmem + 2);
   int* s_off = reinterpret_cast<int*>(s_tmem + 4);
-  // blocks of 64 r that one accumulation chain takes
-  constexpr int kRun = F32 ? kChain : (1 << 30);
   int* s_tile = s_off + (p.E + 1);
   int* s_slot = s_tile + (p.E + 1);      // split products
   int* s_piece = s_bad + 1;
@@ -694,9 +695,9 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
         const uint32_t idesc = idesc_base | (static_cast<uint32_t>(t.mma_n >> 3) << 17);
         // an expert without rows: one stage without MMAs
         const int blocks = FORM == kWgrad ? max(t.blocks, 1) : t.blocks;
-        for (int b0 = 0; b0 < blocks && ok; b0 += kRun, ++it) {
+        for (int b0 = 0; b0 < blocks && ok; b0 += kChain, ++it) {
           const int acc = it & 1;
-          const int b1 = min(blocks, b0 + kRun);
+          const int b1 = min(blocks, b0 + kChain);
           if (!all_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, s_abort, p.status)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TN);
@@ -802,19 +803,28 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
       const int row = FORM == kWgrad ? t.i0 : t.row0 + t.i0;   // output row of column 0
       const int depth = FORM == kWgrad ? group_of<SPLIT>(t) : 0;
       const int slot = SPLIT ? (t.e >> kGroupBits) - 1 : -1;
-      if (F32) {
-        // the tile's chains added in registers, in order
+      const int blocks = FORM == kWgrad ? max(t.blocks, 1) : t.blocks;
+      // the tile's chains are added in registers, in order
+      auto wait_chain = [&] {
+        if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, s_abort, p.status)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto release_chain = [&] {                           // to the issuer's barrier
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty[it & 1], 0));
+      };
+      if (F32 || (SPLIT && slot >= 0)) {
+        // fp32, and pieces: a lane holds a row of the accumulator
         float sum[4][32];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[x][i] = 0.0f;   // also what an expert without rows gets
-        const int blocks = FORM == kWgrad ? max(t.blocks, 1) : t.blocks;
-        for (int b = 0; b < blocks; b += kRun, ++it) {
-          const int acc = it & 1;
-          if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t src = t_lane + static_cast<uint32_t>(acc * TN);
+        for (int b = 0; b < blocks; b += kChain, ++it) {
+          if (!wait_chain()) { ok = false; break; }
+          const uint32_t src = t_lane + static_cast<uint32_t>((it & 1) * TN);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int c = (2 * x + part) * 32;
@@ -826,11 +836,17 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
               for (int i = 0; i < 32; ++i) sum[x][i] += __uint_as_float(v[i]);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty[acc], 0));   // the issuer's barrier
+          release_chain();
         }
         if (!ok) break;
+        uint8_t* buf = os.buf;
+        if (!F32) {
+          // each warp in its half of the two warps' buffer, which the issuer's
+          // last store may still be reading
+          if (elect_one()) bulk_wait_group_read0();
+          if (!os.pair_sync()) { ok = false; break; }
+          buf += (quarter & 1) * OUT_BYTES;
+        }
         if (j < p.n_j) {                                   // warp-uniform
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
@@ -839,16 +855,16 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
               if (elect_one()) bulk_wait_group_read0();
               __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(os.buf + i * 128 + lane * 4) = sum[x][i];
+              for (int i = 0; i < 32; ++i) *reinterpret_cast<float*>(buf + i * 128 + lane * 4) = sum[x][i];
               fence_proxy_async_smem();
               __syncwarp();
               if (SPLIT && slot >= 0) {                    // a whole box: the slot is this piece's alone
                 if (elect_one()) {
-                  tma_store_3d(&p.tmParts, os.buf, j - t.j0, slot * p.slot_i + c, 0);
+                  tma_store_3d(&p.tmParts, buf, j - t.j0, slot * p.slot_i + c, 0);
                   bulk_commit_group();
                 }
                 __syncwarp();
-              } else {
+              } else if constexpr (F32) {
                 flush<FORM, 4>(p, os, j, row + c, depth, t.ni - c, lane);
               }
             }
@@ -857,64 +873,40 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
       } else {
         // 64 columns at a time: 8 x 8 fragments, rounded in pairs and stored
         // transposed
-        const int acc = it & 1;
-        if (!warp_wait(&tfull[acc], (it >> 1) & 1, s_abort, p.status)) { ok = false; break; }
-        tc_fence_after();
-        auto release = [&] {                               // to the issuer's barrier
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty[acc], 0));
-        };
-        if (SPLIT && slot >= 0) {
-          // a piece: fp32 boxes of its warp's own, each warp in its half of the
-          // two warps' buffer, which the issuer's last store may still be reading
-          if (elect_one()) bulk_wait_group_read0();
-          if (!os.pair_sync()) { ok = false; break; }
-          uint8_t* buf = os.buf + (quarter & 1) * OUT_BYTES;
-#pragma unroll 1
-          for (int c = part * 32; c < t.ni && j < p.n_j; c += 64) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(acc * TN + c), v);
-            tmem_ld_wait();
-            if (elect_one()) bulk_wait_group_read0();
-            __syncwarp();
+        float sum[2][64];                                  // [64 columns][lane half][column half][16]
 #pragma unroll
-            for (int i = 0; i < 32; ++i) *reinterpret_cast<uint32_t*>(buf + i * 128 + lane * 4) = v[i];
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (elect_one()) {
-              tma_store_3d(&p.tmParts, buf, j - t.j0, slot * p.slot_i + c, 0);
-              bulk_commit_group();
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 64; ++i) sum[x][i] = 0.0f;
+        for (int b = 0; b < blocks; b += kChain, ++it) {
+          if (!wait_chain()) { ok = false; break; }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int c = part * 64 + (y >> 1) * 128 + (y & 1) * 32;
+            if (c < t.ni && t.blocks > 0) {                // warp-uniform
+              const uint32_t src = t_lane + static_cast<uint32_t>((it & 1) * TN + c);
+              uint32_t v[32];
+              tmem_ld_16x256b_x4(src, v);
+              tmem_ld_16x256b_x4(src + (16u << 16), v + 16);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                sum[y >> 1][(i >> 4) * 32 + (y & 1) * 16 + (i & 15)] += __uint_as_float(v[i]);
             }
-            __syncwarp();
           }
-          release();
-          ++it;
-          continue;
+          release_chain();
         }
-#pragma unroll 1
-        for (int c = part * 64; c < t.ni; c += 128) {
-          uint32_t v[64];                                  // [lane half][column half][16]
-          if (t.blocks > 0) {
-            const uint32_t src = t_lane + static_cast<uint32_t>(acc * TN + c);
-            tmem_ld_16x256b_x4(src, v);
-            tmem_ld_16x256b_x4(src + (16u << 16), v + 32);
-            if (c + 32 < t.mma_n) {
-              tmem_ld_16x256b_x4(src + 32, v + 16);
-              tmem_ld_16x256b_x4(src + 32 + (16u << 16), v + 48);
-            }
-            tmem_ld_wait();
-          } else {                                         // wgrad of an expert without rows
+        if (!ok) break;
+        const int j_box = j & ~63;                         // both warps' 64 columns
+        if (j_box < p.n_j) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) v[i] = 0;
-          }
-          if (c + 128 >= t.ni) release();                  // this warp's last columns are in registers
-          const int j_box = j & ~63;                       // both warps' 64 columns
-          if (j_box < p.n_j) {
+          for (int x = 0; x < 2; ++x) {
+            const int c = part * 64 + x * 128;
+            if (c >= t.ni) break;
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float lo = __uint_as_float(v[2 * i]), hi = __uint_as_float(v[2 * i + 1]);
+              const float lo = sum[x][2 * i], hi = sum[x][2 * i + 1];
               if (OUT == MOE_ELEM_F16) {
                 const __half2 h = __floats2half2_rn(lo, hi);
                 w[i] = *reinterpret_cast<const uint32_t*>(&h);
@@ -936,8 +928,6 @@ __global__ void __launch_bounds__(num_threads(FORM), 1)
             flush<FORM, 2>(p, os, j_box, row + c, depth, t.ni - c, lane);
           }
         }
-        if (part * 64 >= t.ni) release();                  // no columns of its own
-        ++it;
       }
     }
     // the warp's stores complete before the block (and its shared memory) goes

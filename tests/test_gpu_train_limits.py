@@ -92,3 +92,17 @@ def test_long_sums_in_fp32_are_added_in_short_chains(form, sizes, n, k, cut):
     o, ref = product(form, sizes, n, k, BF, F32, cut)
     rel = float((o.double() - ref).norm() / ref.norm())
     assert rel < 16 * 2.0 ** -23, rel
+
+
+@pytest.mark.parametrize("form,rows,n,k,cut", [
+    ("wgrad", 65536, 2048, 2048, None), ("wgrad", 65536, 512, 512, True), ("wgrad", 65536, 512, 512, False),
+    ("forward", 512, 256, 32768, True), ("forward", 512, 256, 32768, False), ("dgrad", 5120, 65536, 2048, None)])
+@pytest.mark.parametrize("dtype", [HF, BF], ids=["f16", "bf16"])
+def test_long_sums_of_one_sign_in_16_bits_are_not_biased(form, rows, n, k, cut, dtype):
+    """Rounding to nearest errs to both sides, half a step at most; truncated
+    sums of one sign lean toward zero together.  They may add a sixteenth of
+    that half step (one chain of 65536 terms adds a whole one in fp16)."""
+    values = lambda *s, **kw: 0.25 + 0.75 * torch.rand(*s, **kw)   # noqa: E731
+    o, ref = product(form, [rows], n, k, dtype, dtype, cut, values)
+    bias = float(((o.double() - ref) / ref).mean())
+    assert abs(bias) < th.half_ulp(dtype) / 16, bias
