@@ -974,13 +974,15 @@ __device__ __forceinline__ void join_step(const JoinParams& p, int step, int ste
   O* out = static_cast<O*>(p.out) +
            ((FORM == kWgrad ? static_cast<int64_t>(e) * p.n_i : static_cast<int64_t>(s_off[e])) + i * h + i0) * p.n_j +
            j * TM + jj;
-  float4 sum[V];
+  // an old weight gradient, loaded ahead and added last: pieces added to it one
+  // by one would each be rounded at its size
+  float4 sum[V], old[V];
 #pragma unroll
   for (int r = 0; r < V; ++r) {
-    sum[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    sum[r] = old[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if constexpr (OUT == MOE_ELEM_F32)
       if (FORM == kWgrad && p.accumulate && i0 + r * kJoinRows < ni)
-        sum[r] = *reinterpret_cast<const float4*>(out + static_cast<int64_t>(r * kJoinRows) * p.n_j);
+        old[r] = *reinterpret_cast<const float4*>(out + static_cast<int64_t>(r * kJoinRows) * p.n_j);
   }
   for (int q = 0; q < pieces; q += U) {
     float4 v[U][V];
@@ -1006,7 +1008,8 @@ __device__ __forceinline__ void join_step(const JoinParams& p, int step, int ste
     if (i0 + r * kJoinRows >= ni) continue;
     O* dst = out + static_cast<int64_t>(r * kJoinRows) * p.n_j;
     if constexpr (OUT == MOE_ELEM_F32) {
-      *reinterpret_cast<float4*>(dst) = sum[r];
+      *reinterpret_cast<float4*>(dst) =
+          make_float4(old[r].x + sum[r].x, old[r].y + sum[r].y, old[r].z + sum[r].z, old[r].w + sum[r].w);
     } else {
       const O w[4] = {Elem<OUT>::from(sum[r].x), Elem<OUT>::from(sum[r].y), Elem<OUT>::from(sum[r].z),
                       Elem<OUT>::from(sum[r].w)};

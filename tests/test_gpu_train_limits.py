@@ -106,3 +106,15 @@ def test_long_sums_of_one_sign_in_16_bits_are_not_biased(form, rows, n, k, cut, 
     o, ref = product(form, [rows], n, k, dtype, dtype, cut, values)
     bias = float(((o.double() - ref) / ref).mean())
     assert abs(bias) < th.half_ulp(dtype) / 16, bias
+
+
+@pytest.mark.parametrize("cut", [True, False], ids=["cut", "uncut"])
+@pytest.mark.parametrize("sizes,n,k", [([20000], 256, 264), ([0, 18000, 700], 512, 512)])
+def test_large_old_weight_gradients_are_rounded_once(sizes, n, k, cut):
+    """An old weight gradient a thousand times the product: the sum is rounded
+    once, by half a unit of 2^-23 at most, and the product's own error (16 x
+    2^-23, above) is a thousandth of that size."""
+    old = 1e3 * max(sizes) ** 0.5
+    o, ref = product("wgrad", sizes, n, k, BF, F32, cut, accumulate=True, old=old)
+    rel = float((o.double() - ref).norm() / ref.norm())
+    assert rel < 2.0 ** -24 * 1.05, rel
