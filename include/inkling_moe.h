@@ -546,6 +546,8 @@ moe_status_t moe_grouped_matmul_wgrad(const moe_grouped_desc_t* desc, const void
  *              not from q.
  *   expert_offsets [n_groups + 1] or NULL: rows at and past
  *              expert_offsets[n_groups] are left alone; NULL: all R rows.
+ *              (No other entry is read.)  A value outside [0, R] is recorded
+ *              in the status word and read as the nearer of the two.
  * dtype MOE_F32 or MOE_BF16; I % 16 == 0 (else MOE_ERR_UNSUPPORTED);
  * perm_slot and topk_w have R entries.  A slot outside [0, R) is recorded in
  * the status word and its row takes weight 0.  Outputs must not overlap

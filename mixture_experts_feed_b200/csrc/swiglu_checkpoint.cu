@@ -145,10 +145,14 @@ struct RowWeight {
   }
 };
 
-__device__ __forceinline__ int64_t live_rows(const int32_t* live, int64_t rows) {
-  if (live == nullptr) return rows;
+// rows that are live; a count outside [0, rows] is recorded and read as the
+// nearer end
+__device__ __forceinline__ int64_t live_rows(const int32_t* live, const RowWeight& rw) {
+  if (live == nullptr) return rw.rows;
   const int64_t n = *live;
-  return n < 0 ? 0 : (n > rows ? rows : n);
+  if (n >= 0 && n <= rw.rows) return n;
+  if (blockIdx.x == 0 && threadIdx.x == 0) record_status(rw.status, DEV_BAD_ROW);
+  return n < 0 ? 0 : rw.rows;
 }
 
 constexpr int kBatch = 4;       // vectors of 8 columns a thread has in flight
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kThreads)
   const int nv = I / 4;                                      // vectors of 8 columns a row
   const int team_size = WIDE ? kThreads : lanes;
   const int me = static_cast<int>(threadIdx.x) & (team_size - 1);
-  const int64_t live_n = live_rows(live_ptr, rw.rows);
+  const int64_t live_n = live_rows(live_ptr, rw);
   const int teams = kThreads / team_size;
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * teams; base < live_n; base += step) {
@@ -232,7 +236,7 @@ __global__ void __launch_bounds__(kThreads)
   const int nv = I / 4;
   const int team_size = WIDE ? kThreads : lanes;
   const int me = static_cast<int>(threadIdx.x) & (team_size - 1);
-  const int64_t live = live_rows(live_ptr, rw.rows);
+  const int64_t live = live_rows(live_ptr, rw);
   const int teams = kThreads / team_size;
   const int64_t step = static_cast<int64_t>(gridDim.x) * teams;
   // every lane of a warp runs the same number of rounds (the shuffles below)

@@ -118,3 +118,41 @@ def test_large_old_weight_gradients_are_rounded_once(sizes, n, k, cut):
     o, ref = product("wgrad", sizes, n, k, BF, F32, cut, accumulate=True, old=old)
     rel = float((o.double() - ref).norm() / ref.norm())
     assert rel < 2.0 ** -24 * 1.05, rel
+
+
+# ------------------------------------------------------------------- SwiGLU
+@pytest.mark.parametrize("last", [-1, -(1 << 31), 41, (1 << 31) - 1])
+def test_swiglu_live_rows_out_of_range_are_recorded(last):
+    """The last offset says how many rows are live: outside [0, R] it is recorded
+    and read as 0 or R, by both passes."""
+    R, I = 40, 32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)   # noqa: E731
+    gu, dh, w = rnd(R, 2 * I), rnd(R, I), torch.rand(R, generator=g, device="cuda")
+    ws = moe.new_status_workspace()
+
+    def both(off):
+        h, q = torch.full_like(dh, 3.0), torch.full((R, 2 * I), 0x33, dtype=torch.uint8, device="cuda")
+        scale = torch.full((R, I // 16), 77, dtype=torch.uint8, device="cuda")
+        dgu, h2, dw = torch.full_like(gu, 3.0), torch.full_like(dh, 3.0), torch.full((R,), 3.0, device="cuda")
+        q8 = q.view(torch.float8_e4m3fn)
+        outs, bad = [h, q, scale], []
+        for call in (lambda: moe.moe_swiglu_checkpoint(gu, off, None, w, h, q8, scale, ws),
+                     lambda: moe.moe_swiglu_backward(q8, scale, dh, off, None, w, dgu, dw, h2, ws)):
+            call()
+            try:
+                moe.read_device_status(ws)
+                bad.append(False)
+            except moe.MoEError:
+                bad.append(True)
+        return outs + [dgu, dw, h2], bad
+
+    offsets = lambda n: torch.tensor([0, 7, n], dtype=torch.int32, device="cuda")   # noqa: E731
+    want, bad = both(offsets(0 if last < 0 else R))
+    assert bad == [False, False]
+    got, bad = both(offsets(last))
+    assert bad == [True, True]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    if last < 0:
+        assert bool((got[0] == 3.0).all()) and bool((got[4] == 0).all())
