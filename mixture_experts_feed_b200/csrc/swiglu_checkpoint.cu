@@ -20,7 +20,10 @@
 // of them are in flight before any is used.  A team of lanes owns a row, so
 // that its weight is looked up once.  Measured on a B200 (65536 rows, I = 2048,
 // bf16): checkpoint 194 us (5.5 TB/s, 84% of the measured copy bandwidth; a
-// thread per 32 columns took 218 us), backward 224 us (6.0 TB/s, 91%; 310 us).
+// thread per 32 columns took 218 us), backward 224 us (6.0 TB/s, 91%; 310 us);
+// fp32: 293 us (6.4 TB/s, 99%) and 394 us (6.2 TB/s, 95%).  Narrow rows stay
+// below that, with fewer loads in flight a lane and a row's look-ups and sums for
+// few columns: I = 64, bf16, 15 us and 19 us (2.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -119,13 +122,31 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t bits) {
   return __half22float2(__half2(h));
 }
 
-// 1 / (1 + e^-g) from t = e^-|g|: both forms divide by a number in [1, 2], so
-// no exponential overflows and the fast division (2 ulp) keeps even the
-// smallest results (it returns 0 for divisors past 2^126).
-__device__ __forceinline__ float sigmoid(float g) {
-  const float t = __expf(-fabsf(g));
-  return __fdividef(g >= 0.0f ? 1.0f : t, 1.0f + t);
-}
+// s = 1 / (1 + e^-g) and c = 1 - s from t = e^-|g|: every quotient divides by a
+// number in [1, 2], so no exponential overflows and even the smallest results
+// keep their digits.
+//   bf16 rows  the fast exponential and division: (12 + 1.2 |g|) 2^-23 relative at
+//              most, far below a bf16 step
+//   fp32 rows  expf (2 ulp): 5 x 2^-23 whatever g is.  The passes have the time
+//              for it, with twice the bytes for the same arithmetic; a division
+//              that rounds correctly would save 3 units of 2^-24 more and take 5%
+//              on the forward pass (65536 rows, I = 2048: 308 us against 293)
+template <typename T> struct Sigmoid {
+  float s, c;
+  __device__ __forceinline__ explicit Sigmoid(float g) {
+    const float t = __expf(-fabsf(g));
+    s = __fdividef(g >= 0.0f ? 1.0f : t, 1.0f + t);
+    c = 1.0f - s;
+  }
+};
+template <> struct Sigmoid<float> {
+  float s, c;
+  __device__ __forceinline__ explicit Sigmoid(float g) {
+    const float t = expf(-fabsf(g)), inv = __fdividef(1.0f, 1.0f + t);   // 2 ulp
+    s = g >= 0.0f ? inv : t * inv;
+    c = g >= 0.0f ? t * inv : inv;
+  }
+};
 
 struct RowWeight {
   const int32_t* perm_slot;
@@ -200,7 +221,7 @@ __global__ void __launch_bounds__(kThreads)
         float out[4];
         if (live)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) out[j] = w * (x[2 * j] * sigmoid(x[2 * j])) * x[2 * j + 1];
+          for (int j = 0; j < 4; ++j) out[j] = w * (x[2 * j] * Sigmoid<T>(x[2 * j]).s) * x[2 * j + 1];
         if (__any_sync(0xffffffffu, top >= 0x7F800000u)) {   // rare: the finite values' top, NaN for the others
           uint32_t t = 0;
           if (live)
@@ -270,9 +291,10 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 4; ++j) {
           const float2 gu = e4m3x2_f32(((j < 2 ? qv[b].x : qv[b].y) >> (16 * (j & 1))) & 0xFFFFu);
           const float g = gu.x * s2, u = gu.y * s2;
-          const float s = sigmoid(g), a = g * s, au = a * u, wd = w * d[j];
+          const Sigmoid<T> sg(g);
+          const float s = sg.s, a = g * s, au = a * u, wd = w * d[j];
           dw = fmaf(d[j], au, dw);
-          o[2 * j] = wd * u * (s * fmaf(g, 1.0f - s, 1.0f));
+          o[2 * j] = wd * u * (s * fmaf(g, sg.c, 1.0f));
           o[2 * j + 1] = wd * a;
           hv[j] = w * au;
         }

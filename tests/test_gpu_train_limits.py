@@ -156,3 +156,38 @@ def test_swiglu_live_rows_out_of_range_are_recorded(last):
         assert torch.equal(a, b)
     if last < 0:
         assert bool((got[0] == 3.0).all()) and bool((got[4] == 0).all())
+
+
+@pytest.mark.parametrize("R,I", [(300, 640), (33, 4096), (1000, 64)])
+def test_swiglu_fp32_rows_keep_fp32_precision(R, I):
+    """fp32 rows, gates out to where e^-g leaves the fp32 range.  In units of 2^-24
+    (half a step): t = e^-|g| is 4 off (expf's 2 ulp), which t / (1 + t) and
+    1 / (1 + t) pass on at most whole; 1 + t adds 1, its reciprocal 4 (2 ulp), the
+    product with t 1: the sigmoid and its complement are 10 off, a 11, h 13 after
+    the weight and u, du 13, a term of d topk_w 13 before the sum.  dg: w dh, u,
+    1 + g (1 - s) and the outer products add 5 to s and to g (1 - s), 25 of the
+    terms' magnitudes."""
+    U, tiny = th.U24, torch.finfo(F32).tiny
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")   # noqa: E731
+    gu, dh, w = rnd(R, 2 * I), rnd(R, I), torch.rand(R, generator=g, device="cuda") + 0.5
+    gu[:, ::2] *= 40.0
+    gu[0, 0], gu[0, 2], gu[0, 4], gu[0, 6] = -88.0, -87.99999, -104.0, 120.0
+    h, q = torch.empty_like(dh), torch.empty(R, 2 * I, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scale, ws = torch.empty(R, I // 16, dtype=torch.uint8, device="cuda"), moe.new_status_workspace()
+    moe.moe_swiglu_checkpoint(gu, None, None, w, h, q, scale, ws)
+    wc = w.double().cpu()[:, None]
+    ref, _ = th.swiglu_exact(gu.double().cpu(), w.double().cpu())
+    th.check(h, ref, 13.01 * U * ref.abs() + tiny, "h")
+    dgu, dw, h2 = torch.empty_like(gu), torch.empty(R, device="cuda"), torch.empty_like(dh)
+    moe.moe_swiglu_backward(q, scale, dh, None, None, w, dgu, dw, h2, ws)
+    v, d = th.dequantise(q, scale), dh.double().cpu()
+    ga, u = v[:, ::2], v[:, 1::2]
+    s, c = torch.sigmoid(ga), torch.sigmoid(-ga)
+    du, hr, terms = wc * d * ga * s, wc * ga * s * u, d * ga * s * u
+    th.check(dgu[:, 1::2], du, 13.01 * U * du.abs() + tiny, "d up")
+    th.check(h2, hr, 13.01 * U * hr.abs() + tiny, "h again")
+    th.check(dgu[:, ::2], wc * d * u * s * (1 + ga * c), 25.01 * U * (wc * d * u).abs() * s * (1 + ga.abs() * c) + tiny,
+             "d gate")
+    th.check(dw, terms.sum(1), (13 + I) * U * terms.abs().sum(1) + tiny, "d topk_w")
+    assert moe.read_device_status(ws) == 0
