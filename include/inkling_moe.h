@@ -604,8 +604,9 @@ moe_status_t moe_norm_workspace_size(int64_t num_tokens, int32_t hidden, size_t*
  *             mean(gy)); dres [T, H] (the residual path's gradient) or NULL
  *   dweight = sum_t dout x^,  dbias = sum_t dout    [H] fp32, in a fixed order
  * x, dout, dres, dx [T, H] and weight [H] in `dtype`; dbias may be NULL.
- * dx may equal x, dout or dres.  T = 0 writes zero dweight and dbias.  A row
- * whose sum of squares passes the fp32 range counts as infinitely long (r = 0).
+ * dx may equal x, dout or dres.  T = 0 writes zero dweight and dbias.  Layer
+ * norm, forward too: a row whose sum of squares passes the fp32 range counts as
+ * infinitely long (r = 0).
  * Calls that share a workspace must be ordered on one stream.
  */
 moe_status_t moe_layer_norm_backward(int64_t num_tokens, int32_t hidden, moe_dtype_t dtype,

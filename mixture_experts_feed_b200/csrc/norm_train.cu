@@ -36,6 +36,7 @@
 // (6.1 TB/s); layer norm forward 8192 x 6144 bf16 45 us (4.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -48,6 +49,9 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+// RMSNorm rows whose squares pass the fp32 range (moe_rmsnorm sums in fp64) are
+// summed again at this scale: values to 2^128 then have squares to 2^116.
+constexpr float kDown = 0x1p-70f;
 
 __device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
@@ -87,6 +91,14 @@ __device__ __forceinline__ float2 row_stats(const T* row, int H, float eps) {
     v = fmaf(d, d, v);
   }
   const float var = block_sum2(v, 0.0f).x / H;
+  if (!LAYER && !(var <= FLT_MAX)) {        // uniform over the block
+    v = 0.0f;
+    for (int c = threadIdx.x; c < H; c += kThreads) {
+      const float d = to_f32(row[c]) * kDown;
+      v = fmaf(d, d, v);
+    }
+    return make_float2(0.0f, kDown / sqrtf(block_sum2(v, 0.0f).x / H + eps * kDown * kDown));
+  }
   return make_float2(mean, 1.0f / sqrtf(var + eps));
 }
 
@@ -165,8 +177,9 @@ __host__ __device__ constexpr int stages_of(bool layer, int arrays) { return lay
 // enough.  One or two values go by butterflies; four are scattered over the
 // lanes as they are summed (the first exchange leaves each lane 2 of them, the
 // second 1, three more steps finish: 6 shuffles instead of 20), summed over
-// the warps side by side, and broadcast.
-template <int N>
+// the warps side by side, and broadcast.  ONE: a call that this team alone makes,
+// past a barrier of its own.
+template <int N, bool ONE = false>
 __device__ __forceinline__ void team_sum(float (&v)[N], int tpr, float (*s_red)[4 * kMaxWarps], int& buf) {
   static_assert(N == 1 || N == 2 || N == 4, "");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wpr = tpr >> 5;
@@ -179,7 +192,8 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int tpr, float (*s_red)[
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) s_red[buf][warp * N + i] = v[i];
-    __syncthreads();
+    if (ONE) asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x) / tpr), "r"(tpr) : "memory");
+    else __syncthreads();
     constexpr int W = kMaxWarps / N;
     const int w = lane & (W - 1);
     const float* part = s_red[buf] + (warp - warp % wpr + w) * N;
@@ -403,9 +417,27 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
       s[LAYER ? 3 : 0] = tm.row_sum(after);
     }
     team_sum<LAYER ? 4 : 2>(s, tpr, s_red, buf);
-    // dx = r gy - r mean(gy) - k x',  k = r^3 mean(gy x')
-    const float r = rsqrtf(s[0] * inv_h + eps);
-    const float k = -r * (r * (r * (s[1] * inv_h)));
+    // dx = r gy - r mean(gy) + k x^,  k = -r mean(gy x^),  x^ = r x'
+    float r = rsqrtf(s[0] * inv_h + eps), rs = r;
+    if (!LAYER && !(s[0] <= FLT_MAX)) {     // uniform over the team
+      sxx = sgx = 0;
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const uint4 xq = read(0, j), gq = read(1, j);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const f32x2 xc = mul2(Vec<T>::pair(xq, i), pack2(kDown, kDown));
+          sxx = fma2(xc, xc, sxx);
+          sgx = fma2(mul2(Vec<T>::pair(gq, i), Vec<T>::pair(wq[j], i)), xc, sgx);
+        }
+      }
+      float b[2] = {sum2(sxx), sum2(sgx)};
+      team_sum<2, true>(b, tpr, s_red, buf);
+      s[1] = b[1];
+      rs = rsqrtf(b[0] * inv_h + eps * kDown * kDown);
+      r = rs * kDown;
+    }
+    const float k = -r * (rs * (s[1] * inv_h));
     const float m1 = LAYER ? -r * (s[LAYER ? 2 : 0] * inv_h) : 0.0f;
     const f32x2 r2 = pack2(r, r), k2 = pack2(k, k), m12 = pack2(m1, m1);
     if (t < rows)
@@ -421,9 +453,10 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
             f32x2 xc = Vec<T>::pair(xq, i);
             if (LAYER) xc = add2(xc, neg_mean);
             const f32x2 g = Vec<T>::pair(gq, i);
-            aw[j][i] = fma2(g, mul2(xc, r2), aw[j][i]);
+            const f32x2 xh = mul2(xc, r2);
+            aw[j][i] = fma2(g, xh, aw[j][i]);
             if (LAYER) ab[j][i] = add2(ab[j][i], g);
-            f32x2 v = LAYER ? fma2(xc, k2, m12) : mul2(xc, k2);
+            f32x2 v = LAYER ? fma2(xh, k2, m12) : mul2(xh, k2);
             v = fma2(mul2(g, Vec<T>::pair(wq[j], i)), r2, v);
             d[i] = RES ? add2(v, Vec<T>::pair(dq, i)) : v;
           }

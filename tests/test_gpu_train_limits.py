@@ -191,3 +191,38 @@ def test_swiglu_fp32_rows_keep_fp32_precision(R, I):
              "d gate")
     th.check(dw, terms.sum(1), (13 + I) * U * terms.abs().sum(1) + tiny, "d topk_w")
     assert moe.read_device_status(ws) == 0
+
+
+# -------------------------------------------------------------------- norms
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(9, 64), (301, 256), (300, 1024), (20, 6144), (7, 8192), (5, 1001), (3, 16384)])
+def test_rmsnorm_backward_of_rows_past_the_fp32_squares(T, H, dtype):
+    """Rows of 1e20 to 1e37, whose squares pass the fp32 range, between ordinary
+    ones: moe_rmsnorm, which sums in fp64, gives them finite results, so they
+    have gradients like any other row's.  Bounds as of ordinary rows."""
+    eps = 1e-5
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")   # noqa: E731
+    x = rnd(T, H)
+    for i, scale in enumerate((1e20, 1e28, 1e37)):
+        x[i::7] *= scale
+    x, w, do, dres = x.to(dtype), (1 + 0.3 * rnd(H)).to(dtype), rnd(T, H).to(dtype), rnd(T, H).to(dtype)
+    xh, r, _ = th.norm_exact(x, w, None, eps, False)
+    c, dxh = th.norm_errors(x, xh, r, H, False)
+    dod, mean = do.double(), lambda v: v.mean(1, keepdim=True)   # noqa: E731
+    gy = dod * w.double()
+    m2 = mean(gy * xh)
+    ref0 = r * (gy - xh * m2)
+    err = r * (c * gy.abs() + xh.abs() * (c * mean((gy * xh).abs()) + mean(gy.abs() * dxh)) + dxh * m2.abs() +
+               c * (xh * m2).abs()) + c * ref0.abs()
+    dw_ref = (dod * xh).sum(0)
+    dw_tol = (dod.abs() * dxh).sum(0) + (T / 148 + 592 + 32) * th.U24 * (dod * xh).abs().sum(0) + 1e-30
+    ws = moe.new_norm_workspace(T, H)
+    for res in (None, dres):
+        dx, dw = torch.full_like(x, 9.0), torch.empty(H, device="cuda")
+        moe.moe_rmsnorm_backward(x, w, do, dx, dw, ws, eps, dres=res)
+        ref = ref0 if res is None else ref0 + res.double()
+        # results of the largest rows reach the subnormals: their step, a few times
+        small = 2.0 ** (-133 if dtype == BF else -149) * 4
+        th.check(dx, ref, (th.half_ulp(dtype) + 2 * th.U24) * ref.abs() + err + small, f"dx {T} {H}")
+        th.check(dw, dw_ref, dw_tol, "dweight")
