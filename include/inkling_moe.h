@@ -480,7 +480,7 @@ typedef enum { MOE_ELEM_F32 = 0, MOE_ELEM_BF16 = 1, MOE_ELEM_F16 = 2 } moe_elem_
 typedef struct {
   int64_t rows;       /* R: rows of the row operands (capacity; < 2^31) */
   int32_t n_groups;   /* E, 1..1024 */
-  int32_t n, k;       /* out and in features */
+  int32_t n, k;       /* out and in features, at most 2^24 */
   int32_t dtype;      /* moe_elem_t of every operand */
   int32_t out_dtype;  /* moe_elem_t of the output: dtype, or MOE_ELEM_F32 */
 } moe_grouped_desc_t;
@@ -515,9 +515,10 @@ moe_status_t moe_grouped_workspace_size(const moe_grouped_desc_t* desc, size_t* 
  * SMs idle (few columns, few rows or few experts) and the sum is long (more
  * than 47 x 64 terms), tiles may be cut along the sum and a second launch adds
  * the parts, in a fixed order.  fp32 operands and other sizes run on the CUDA
- * cores.  An fp16 output past 65504 becomes an infinity.  Outputs must not
- * overlap operands.  R = 0: the first two launch nothing; the third still
- * reads expert_offsets and writes dW.
+ * cores.  An fp16 output past 65504 becomes an infinity (in the caller's own
+ * output, so it is not recorded in the status word: with scaled losses it is
+ * an ordinary event).  Outputs must not overlap operands.  R = 0: the first two
+ * launch nothing; the third still reads expert_offsets and writes dW.
  */
 moe_status_t moe_grouped_matmul(const moe_grouped_desc_t* desc, const void* a, const void* w,
                                 const int32_t* expert_offsets, void* out, void* workspace,

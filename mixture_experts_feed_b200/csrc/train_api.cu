@@ -30,7 +30,10 @@ moe_status_t check_grouped(const moe_grouped_desc_t* d) {
   if (d->dtype != MOE_ELEM_F32 && d->dtype != MOE_ELEM_BF16 && d->dtype != MOE_ELEM_F16)
     return MOE_ERR_INVALID_ARG;
   if (d->out_dtype != d->dtype && d->out_dtype != MOE_ELEM_F32) return MOE_ERR_INVALID_ARG;
-  if (d->rows >= (int64_t{1} << 31) || d->n_groups > 1024) return MOE_ERR_UNSUPPORTED;
+  // past 2^24 features the kernels' tile counts (the fewest rows and columns a
+  // tile has: 1 x 16) would leave 32 bits
+  if (d->rows >= (int64_t{1} << 31) || d->n_groups > 1024 || d->n > (1 << 24) || d->k > (1 << 24))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
