@@ -349,6 +349,35 @@ __global__ void __launch_bounds__(kMaxTeam, 2)
   copy_wait<0>();
 }
 
+// A thread's slots of a row (x, then dout, each VPT vectors `stride` apart):
+// b += its sums of (x 2^-70)^2 and gy x 2^-70; and x times a power of two.
+template <typename T, int VPT>
+__device__ __forceinline__ void scaled_sums(const uint4* slots, const uint4 (&wq)[VPT], int stride, float (&b)[2]) {
+  f32x2 sxx = 0, sgx = 0;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const uint4 xq = slots[j * stride], gq = slots[(VPT + j) * stride];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::P; ++i) {
+      const f32x2 x = mul2(Vec<T>::pair(xq, i), pack2(kDown, kDown));
+      sxx = fma2(x, x, sxx);
+      sgx = fma2(mul2(Vec<T>::pair(gq, i), Vec<T>::pair(wq[j], i)), x, sgx);
+    }
+  }
+  b[0] += sum2(sxx);
+  b[1] += sum2(sgx);
+}
+template <typename T, int VPT> __device__ __forceinline__ void scale_slots(uint4* slots, int stride, float by) {
+#pragma unroll 1
+  for (int j = 0; j < VPT; ++j) {
+    const uint4 q = slots[j * stride];
+    f32x2 x[Vec<T>::P];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::P; ++i) x[i] = mul2(Vec<T>::pair(q, i), pack2(by, by));
+    slots[j * stride] = Vec<T>::put(x);
+  }
+}
+
 template <typename T, int VPT, bool LAYER, bool RES>
 __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
     norm_backward_rows_kernel(const T* x_, const T* __restrict__ w_, const T* dout_, const T* dres_, T* dx_,
@@ -417,29 +446,28 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
       s[LAYER ? 3 : 0] = tm.row_sum(after);
     }
     team_sum<LAYER ? 4 : 2>(s, tpr, s_red, buf);
-    // dx = r gy - r mean(gy) + k x^,  k = -r mean(gy x^),  x^ = r x'
-    float r = rsqrtf(s[0] * inv_h + eps), rs = r;
+    // dx = r gy - r mean(gy) + k x',  k = -r^3 mean(gy x')
+    float r = rsqrtf(s[0] * inv_h + eps), rx = r;
+    float k = -r * (r * (r * (s[1] * inv_h)));
     if (!LAYER && !(s[0] <= FLT_MAX)) {     // uniform over the team
-      sxx = sgx = 0;
-#pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const uint4 xq = read(0, j), gq = read(1, j);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const f32x2 xc = mul2(Vec<T>::pair(xq, i), pack2(kDown, kDown));
-          sxx = fma2(xc, xc, sxx);
-          sgx = fma2(mul2(Vec<T>::pair(gq, i), Vec<T>::pair(wq[j], i)), xc, sgx);
-        }
-      }
-      float b[2] = {sum2(sxx), sum2(sgx)};
+      // RMSNorm, squares past the fp32 range: summed again at 2^-70.  The thread's
+      // own slots of the row are then scaled to values around 1 (by a power of two,
+      // so exactly), x^ = rx x', and k keeps its digits.
+      uint4* x_slots = tm.mine + stage * tm.stage_vecs;
+      float b[2] = {0.0f, 0.0f};
+      scaled_sums<T, VPT>(x_slots, wq, static_cast<int>(blockDim.x), b);
       team_sum<2, true>(b, tpr, s_red, buf);
-      s[1] = b[1];
-      rs = rsqrtf(b[0] * inv_h + eps * kDown * kDown);
-      r = rs * kDown;
+      if (b[0] <= FLT_MAX) {                // else an infinity or NaN in the row
+        const float rs = rsqrtf(b[0] * inv_h + eps * kDown * kDown);
+        const float p = __uint_as_float(__float_as_uint(rs) & 0x7F800000u);
+        r = rs * kDown;
+        rx = rs / p;
+        k = -r * (rx * (rs * (b[1] * inv_h)));
+        scale_slots<T, VPT>(x_slots, static_cast<int>(blockDim.x), kDown * p);
+      }
     }
-    const float k = -r * (rs * (s[1] * inv_h));
     const float m1 = LAYER ? -r * (s[LAYER ? 2 : 0] * inv_h) : 0.0f;
-    const f32x2 r2 = pack2(r, r), k2 = pack2(k, k), m12 = pack2(m1, m1);
+    const f32x2 r2 = pack2(r, r), rx2 = LAYER ? r2 : pack2(rx, rx), k2 = pack2(k, k), m12 = pack2(m1, m1);
     if (t < rows)
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
@@ -453,10 +481,9 @@ __global__ void __launch_bounds__(max_threads(VPT), min_blocks(VPT))
             f32x2 xc = Vec<T>::pair(xq, i);
             if (LAYER) xc = add2(xc, neg_mean);
             const f32x2 g = Vec<T>::pair(gq, i);
-            const f32x2 xh = mul2(xc, r2);
-            aw[j][i] = fma2(g, xh, aw[j][i]);
+            aw[j][i] = fma2(g, mul2(xc, rx2), aw[j][i]);
             if (LAYER) ab[j][i] = add2(ab[j][i], g);
-            f32x2 v = LAYER ? fma2(xh, k2, m12) : mul2(xh, k2);
+            f32x2 v = LAYER ? fma2(xc, k2, m12) : mul2(xc, k2);
             v = fma2(mul2(g, Vec<T>::pair(wq[j], i)), r2, v);
             d[i] = RES ? add2(v, Vec<T>::pair(dq, i)) : v;
           }
