@@ -616,7 +616,8 @@ def _stream_on(dev: int, stream):
 @dataclass(frozen=True)
 class GroupedMatmul:
     """Sizes of a matrix product grouped by expert: row operands of ``rows``
-    rows, weights ``[E, n, k]``; ``out_dtype`` is ``dtype`` or fp32."""
+    rows, weights ``[E, n, k]`` (n and k at most 2^24); ``out_dtype`` is
+    ``dtype`` or fp32."""
     rows: int
     E: int
     n: int

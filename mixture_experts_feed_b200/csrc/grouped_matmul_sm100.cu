@@ -47,9 +47,9 @@
 // along r into pieces, each a tile of its own whose accumulator goes to a slot
 // of the workspace, and a second kernel adds a tile's slots in order:
 // reproducible, where adds to memory would not be.  Measured (us, cut / whole):
-// dW of one expert of 16384 rows, 256 x 256, 24 / 84; of 8192 rows, 1024 x 1024,
-// 34 / 50; 65536 rows all in one of 64 experts, 512 x 512, 59 / 305; 249 rows,
-// k = 4096, n = 1024, 23 / 29.  Now 12 us of launches and drain, the loads, and the
+// dW of one expert of 16384 rows, 256 x 256, 19 / 79; of 8192 rows, 1024 x 1024,
+// 29 / 44; 65536 rows all in one of 64 experts, 512 x 512, 54 / 303; 249 rows,
+// k = 4096, n = 1024, 18 / 25.  Bound now by launches and drain, the loads, and the
 // slots through L2.
 //
 // Roles (one CTA an SM): warp 0 loads, warp 1 allocates tensor memory and
@@ -60,18 +60,18 @@
 //
 // What bounds it.  A block of 64 r costs a pair 512 clocks of MMA at N = 256
 // and brings 32 KB to each SM, about what the TMA unit moves in that time (64
-// bytes a clock, a row of 128 bytes at a time): 8192^3 in bf16 takes 0.92 M
-// clocks, its MMAs' own time.  To get there the loading and issuing warps run
-// converged and elect a lane for the instruction itself (with one lane in the
-// loop every operand went through the vector registers, 730 clocks a block),
-// nothing but the MMAs' operands lies between two tiles (tiles come from a
+// bytes a clock, a row of 128 bytes at a time): 8192^3 in bf16 keeps the tensor
+// pipe busy 95% of a launch's 0.97 M clocks.  To get there the loading and issuing
+// warps run converged and elect a lane for the instruction itself (with one lane
+// in the loop every operand went through the vector registers, 730 clocks a
+// block), nothing but the MMAs' operands lies between two tiles (tiles come from a
 // queue), and accumulators are handed back with a light arrival.  From there
-// the 1 kW power limit sets the clock.  Measured on a B200, back to back (SM
-// clock 1.0 to 1.3 GHz): 8192^3 1294 TFLOP/s (the library product 1413);
-// 65536 rows of 128 experts, n = 4096, k = 6144, fp32 dx, 965 TFLOP/s at 2.45
-// TB/s; 24576 rows of 64 experts, n = k = 2048: forward 930, dW 885 TFLOP/s
-// at 3.2 TB/s.  DRAM traffic is the algorithm's (forward: 638 MB read for 637,
-// dW 201 for 201).  Six decoded rows (50 MB of weights) take 15 us.
+// the 1 kW power limit sets the clock.  Measured on B200s, back to back (SM
+// clock 1.0 to 1.3 GHz): 8192^3 1279 TFLOP/s (the library product 1343 to 1366);
+// 65536 rows of 128 experts, n = 4096, k = 6144, fp32 dx, 947 to 990 TFLOP/s at
+// 2.5 TB/s; 24576 rows of 64 experts, n = k = 2048: forward 892 to 920, dW 860 to
+// 893 TFLOP/s at 3.1 TB/s.  DRAM traffic is the algorithm's (forward: 638 MB read
+// for 637, dW 201 for 201).  Six decoded rows (50 MB of weights) take 15 us.
 #include <algorithm>
 #include <atomic>
 
@@ -1143,12 +1143,11 @@ cudaError_t launch_out(int form, const ProductParams& p, float* parts, int64_t m
 //                   a tile, and r has at least 48 blocks (256 rows, n = 2560 to
 //                   256 columns 22 us cut, 24 whole; n = 2048 21 both ways)
 //   wgrad           groups of even length leave half of the pairs without a tile
-//                   and have 48 blocks each (4096 rows, 256 x 256: 22 us cut, 31
-//                   whole; 2048 rows 22 both ways), or kSkewedRows rows,
-//                   few tiles a group, and possibly most rows in one group
-//                   (16 groups of 32768 rows, 512 x 512: even 31 us cut, 29 whole;
-//                   longest 9592 rows 45 and 57.  64 of 65536: even 47 and
-//                   45, all rows in one 59 and 305)
+//                   and have 48 blocks each (4096 rows, 256 x 256: 16 us cut, 24
+//                   whole; 3136 rows 16 and 20), or kSkewedRows rows, few tiles a
+//                   group, and possibly most rows in one group (16 groups of 32768
+//                   rows, 512 x 512: even 23 us cut, 21 whole; longest 9592 rows 41
+//                   and 53.  64 of 65536: even 41 and 43, all rows in one 54 and 303)
 struct Slots { int count, i, j; };
 Slots split_slots(int form, int64_t rows, int E, int n, int k) {
   constexpr int64_t kMinBlocks = 6 * kMinPiece;

@@ -31,9 +31,10 @@
 // threads measured slower: 142 us where this takes 74), and layer norm's four
 // sums are scattered over the lanes as they are added.  Measured on a B200:
 // RMSNorm backward with residual, 8192 x 6144 bf16, 74 us (5.4 TB/s, 83% of the
-// measured copy bandwidth); layer norm backward 80 us there (3.8 TB/s: 30
+// measured copy bandwidth); layer norm backward 80 to 84 us there (3.7 TB/s: 30
 // instructions an element) and 21 us on 4096 x 2048; 8192 x 4096 fp32 66 us
-// (6.1 TB/s); layer norm forward 8192 x 6144 bf16 45 us (4.4 TB/s).
+// (6.1 TB/s), with residual 84 us (6.4 TB/s); layer norm forward 8192 x 6144 bf16
+// 45 us (4.4 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
